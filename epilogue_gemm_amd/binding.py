@@ -33,6 +33,19 @@ class Extras(ctypes.Structure):
     _fields_ = [("col_scale", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out_scale", ctypes.c_void_p)]
 
 
+class _PagedCache(ctypes.Structure):
+    """struct gemm_epi_paged_cache (include/gemm_epi_decode.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class _PageTable(ctypes.Structure):
+    """struct gemm_epi_page_table (include/gemm_epi_decode.h)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("ld", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("batch", ctypes.c_int64)]
+
+
 class GemmEpiError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -95,6 +108,21 @@ def load_library(path: str = LIB_PATH):
     lib.gemm_epi_num_configs.restype = i32
     lib.gemm_epi_plan_describe.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.gemm_epi_plan_describe.restype = cp
+    # the operators of a decode step (include/gemm_epi_decode.h)
+    sz, f32 = ctypes.c_size_t, ctypes.c_float
+    pc, pt = ctypes.POINTER(_PagedCache), ctypes.POINTER(_PageTable)
+    lib.gemm_epi_rmsnorm.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, f32, i32, i32, vp]
+    lib.gemm_epi_rmsnorm.restype = i32
+    lib.gemm_epi_lora.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64, i64, i64, i64, i64, i32, vp, sz, vp]
+    lib.gemm_epi_lora.restype = i32
+    lib.gemm_epi_lora_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.gemm_epi_lora_workspace_size.restype = sz
+    lib.gemm_epi_cache_append.argtypes = [pc, pt, vp, i64, vp, i64, vp, i64, i32, vp]
+    lib.gemm_epi_cache_append.restype = i32
+    lib.gemm_epi_attention_decode.argtypes = [pc, pt, vp, i64, vp, i64, i64, i32, vp, sz, vp]
+    lib.gemm_epi_attention_decode.restype = i32
+    lib.gemm_epi_attention_decode_workspace_size.argtypes = [pc, i64, i64, i64]
+    lib.gemm_epi_attention_decode_workspace_size.restype = sz
     # measurement helpers (include/gemm_epi_probes.h)
     lib.gemm_epi_probe_hbm_read.argtypes = [vp, ctypes.c_size_t, vp, vp]
     lib.gemm_epi_probe_hbm_read.restype = i32
@@ -229,6 +257,281 @@ def attention_fwd(q, k, v, o, causal=False, stream=None):
                                 _dtype_name(q), causal, s)
     if st != OK:
         raise GemmEpiError("gemm_epi_attention_fwd", st)
+
+
+# ---- the operators of a decode step (include/gemm_epi_decode.h) --------------
+
+def gemm_epi_rmsnorm(X, ldx, R, ldr, W, H, ldh, Y, ldy, y_scale, rows, cols, eps, dtype, out_dtype, stream) -> int:
+    return load_library().gemm_epi_rmsnorm(X, ldx, R, ldr, W, H, ldh, Y, ldy, y_scale, rows, cols, eps,
+                                           DTYPES[dtype], DTYPES[out_dtype], stream)
+
+
+def gemm_epi_lora(X, ldx, A, B, scale, ids, R, ldr, C, ldc, M, N, K, rank, adapters, dtype, ws, ws_bytes,
+                  stream) -> int:
+    return load_library().gemm_epi_lora(X, ldx, A, B, scale, ids, R, ldr, C, ldc, M, N, K, rank, adapters,
+                                        DTYPES[dtype], ws, ws_bytes, stream)
+
+
+def gemm_epi_lora_workspace_size(M, N, K, rank, adapters) -> int:
+    return int(load_library().gemm_epi_lora_workspace_size(M, N, K, rank, adapters))
+
+
+def paged_cache_struct(k, v, k_scale, v_scale, num_pages, page_size, heads, head_dim, dtype):
+    """A gemm_epi_paged_cache of pointers and sizes (for the two calls below)."""
+    return _PagedCache(k, v, k_scale, v_scale, num_pages, page_size, heads, head_dim, DTYPES[dtype])
+
+
+def page_table_struct(pages, ld, width, lens, batch):
+    """A gemm_epi_page_table of pointers and sizes."""
+    return _PageTable(pages, ld, width, lens, batch)
+
+
+def gemm_epi_cache_append(cache, table, K, ldk, V, ldv, starts, tokens, dtype, stream) -> int:
+    return load_library().gemm_epi_cache_append(cache, table, K, ldk, V, ldv, starts, tokens, DTYPES[dtype], stream)
+
+
+def gemm_epi_attention_decode(cache, table, Q, ldq, O, ldo, q_heads, dtype, ws, ws_bytes, stream) -> int:
+    return load_library().gemm_epi_attention_decode(cache, table, Q, ldq, O, ldo, q_heads, DTYPES[dtype], ws,
+                                                    ws_bytes, stream)
+
+
+def gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads) -> int:
+    return int(load_library().gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads))
+
+
+def _device_check(name, t, index):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {index}")
+
+
+def _rows(name, t, dtype, shape, index):
+    """Checks a tensor whose first axis may be strided and whose other axes
+    are packed, and returns the elements between its rows."""
+    _device_check(name, t, index)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    width = 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: only the first axis may be strided")
+        width *= shape[i]
+    return st[0] if shape[0] > 1 else width  # one row has no distance to a next one
+
+
+def _packed(name, t, dtype, shape, index):
+    _device_check(name, t, index)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _format(name, t):
+    n = _dtype_name(t)
+    if n not in ("f16", "bf16"):
+        raise ValueError(f"{name}: dtype {t.dtype}; expected float16 or bfloat16")
+    return n
+
+
+def _stream_handle(torch, stream, index):
+    """hipStream_t of `stream` (of the current device), or of torch's current
+    stream."""
+    if stream is None:
+        return _current_stream_handle(torch)
+    if stream.device.index != index:
+        raise ValueError(f"stream: on device {stream.device.index}, the current device is {index}")
+    return stream.cuda_stream
+
+
+def _workspace(torch, workspace, need, index, stream):
+    """(pointer, bytes) of the caller's workspace, or of one from torch's
+    allocator on the stream of the call."""
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+    else:
+        _device_check("workspace", workspace, index)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e-6, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight over the last
+    axis of [rows, cols] tensors of one 16-bit format (the rows may be
+    strided); ``residual_out`` receives h, and may be ``residual`` or ``x``
+    itself.  ``y`` is of the same format, or float8_e4m3fn with
+    ``y_scale`` ([rows] float32) receiving each row's scale.  Enqueued on
+    torch's current stream (or `stream`), not synchronised."""
+    import torch
+
+    index = torch.cuda.current_device()
+    if x.dim() != 2:
+        raise ValueError("x: expected a 2-d tensor [rows, cols]")
+    fmt, shape, dt = _format("x", x), x.shape, x.dtype
+    rows, cols = shape
+    ldx = _rows("x", x, dt, shape, index)
+    w = _packed("weight", weight, dt, (cols,), index)
+    r = h = s = None
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _rows("residual", residual, dt, shape, index)
+        r = residual.data_ptr()
+    if residual_out is not None:
+        ldh = _rows("residual_out", residual_out, dt, shape, index)
+        h = residual_out.data_ptr()
+    out = fmt
+    if y_scale is not None:
+        out = "fp8"
+        s = _packed("y_scale", y_scale, torch.float32, (rows,), index)
+    ldy = _rows("y", y, torch.float8_e4m3fn if y_scale is not None else dt, shape, index)
+    st = gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, s, rows, cols, eps, fmt, out,
+                          _stream_handle(torch, stream, index)) if rows else OK
+    if st != OK:
+        raise GemmEpiError("gemm_epi_rmsnorm", st)
+
+
+def lora_workspace_size(M, N, K, rank, adapters) -> int:
+    """Bytes of workspace ``lora`` uses for these sizes."""
+    return gemm_epi_lora_workspace_size(M, N, K, rank, adapters)
+
+
+def lora(x, a, b, ids, c, scale=None, residual=None, workspace=None, stream=None):
+    """c[m] = residual[m] + scale[i] (x[m] a[i]^T) b[i]^T with i = ids[m]; a
+    row whose id is outside [0, adapters) has no adapter.  x [M, K], c and
+    residual [M, N] (rows may be strided; ``residual`` may be ``c`` itself, or
+    None for 0), a [adapters, rank, K] and b [adapters, N, rank], all of one
+    16-bit format; ids [M] int32, scale [adapters] float32 or None for 1.
+    ``workspace``: an optional CUDA tensor of ``lora_workspace_size`` bytes,
+    else one is allocated.  With residual None, c is what ``Plan.run`` of the
+    projection takes as its residual."""
+    import torch
+
+    index = torch.cuda.current_device()
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x, a, b: expected tensors [M, K], [adapters, rank, K] and [adapters, N, rank]")
+    fmt, dt = _format("x", x), x.dtype
+    M, K = x.shape
+    adapters, rank = a.shape[:2]
+    N = b.shape[1]
+    ldx = _rows("x", x, dt, (M, K), index)
+    pa = _packed("a", a, dt, (adapters, rank, K), index)
+    pb = _packed("b", b, dt, (adapters, N, rank), index)
+    pi = _packed("ids", ids, torch.int32, (M,), index)
+    ldc = _rows("c", c, dt, (M, N), index)
+    ps = None if scale is None else _packed("scale", scale, torch.float32, (adapters,), index)
+    pr, ldr = None, 0
+    if residual is not None:
+        ldr = _rows("residual", residual, dt, (M, N), index)
+        pr = residual.data_ptr()
+    if M == 0:
+        return
+    s = _stream_handle(torch, stream, index)
+    ws, nbytes = _workspace(torch, workspace, gemm_epi_lora_workspace_size(M, N, K, rank, adapters)
+                            if workspace is None else 0, index, stream)
+    st = gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
+                       ws, nbytes, s)
+    if st != OK:
+        raise GemmEpiError("gemm_epi_lora", st)
+
+
+class PagedCache:
+    """The paged key-value cache of one layer over the caller's tensors: k and
+    v [num_pages, heads, page_size, head_dim] in float16, bfloat16 or
+    float8_e4m3fn, the latter with k_scale and v_scale [num_pages, heads,
+    page_size] float32.  ``append`` and ``attend`` enqueue on torch's current
+    stream (or the given one) and return without synchronising.
+
+    Both take ``pages`` [batch, width] int32 (rows may be strided; an entry
+    outside [0, num_pages) is no page) and ``lens`` [batch] int32, the tokens
+    each sequence holds, those of the current step included."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+
+        if k.dim() != 4:
+            raise ValueError("k: expected a 4-d tensor [num_pages, heads, page_size, head_dim]")
+        fmt = _dtype_name(k)
+        if fmt not in ("f16", "bf16", "fp8"):
+            raise ValueError(f"k: dtype {k.dtype}; expected float16, bfloat16 or float8_e4m3fn")
+        self.device_index = k.get_device()
+        shape = k.shape
+        pk = _packed("k", k, k.dtype, shape, self.device_index)
+        pv = _packed("v", v, k.dtype, shape, self.device_index)
+        if (fmt == "fp8") != (k_scale is not None) or (fmt == "fp8") != (v_scale is not None):
+            raise ValueError("k_scale, v_scale: for a float8_e4m3fn cache, and only then")
+        pks = pvs = None
+        if fmt == "fp8":
+            pks = _packed("k_scale", k_scale, torch.float32, shape[:3], self.device_index)
+            pvs = _packed("v_scale", v_scale, torch.float32, shape[:3], self.device_index)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = shape
+        self._struct = paged_cache_struct(pk, pv, pks, pvs, shape[0], shape[2], shape[1], shape[3], fmt)
+
+    def _table(self, torch, pages, lens):
+        index = torch.cuda.current_device()
+        if index != self.device_index:
+            raise ValueError(f"the cache is on device {self.device_index}, the current device is {index}")
+        if pages.dim() != 2:
+            raise ValueError("pages: expected a 2-d tensor [batch, width]")
+        batch, width = pages.shape
+        ld = _rows("pages", pages, torch.int32, pages.shape, index)
+        return page_table_struct(pages.data_ptr(), ld, width, _packed("lens", lens, torch.int32, (batch,), index),
+                                 batch)
+
+    def append(self, k, v, pages, lens, starts=None, stream=None):
+        """Writes the rows k and v [tokens, heads, head_dim] (rows may be
+        strided) to their sequences' last positions.  ``starts`` [batch + 1]
+        int32: the rows of sequence i are starts[i] .. starts[i + 1] - 1, rows
+        from starts[batch] on are ignored; None: one row a sequence."""
+        import torch
+
+        table = self._table(torch, pages, lens)
+        index = self.device_index
+        fmt = _format("k", k)
+        shape = (k.shape[0], self.heads, self.head_dim)
+        ldk, ldv = _rows("k", k, k.dtype, shape, index), _rows("v", v, k.dtype, shape, index)
+        p = None if starts is None else _packed("starts", starts, torch.int32, (table.batch + 1,), index)
+        st = gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv, p, shape[0], fmt,
+                                   _stream_handle(torch, stream, index))
+        if st != OK:
+            raise GemmEpiError("gemm_epi_cache_append", st)
+
+    def workspace_size(self, q_heads, pages) -> int:
+        """Bytes of workspace ``attend`` uses for this page table."""
+        return gemm_epi_attention_decode_workspace_size(self._struct, pages.shape[0], pages.shape[1], q_heads)
+
+    def attend(self, q, o, pages, lens, workspace=None, stream=None):
+        """o[i, h] = attention of query q[i, h] over the tokens of sequence i
+        (0 where there are none).  q and o [batch, q_heads, head_dim] (rows
+        may be strided), float16 or bfloat16, the cache's format unless that
+        is float8_e4m3fn.  ``workspace``: an optional CUDA tensor of
+        ``workspace_size`` bytes, else one is allocated."""
+        import torch
+
+        table = self._table(torch, pages, lens)
+        index = self.device_index
+        fmt = _format("q", q)
+        if q.dim() != 3:
+            raise ValueError("q: expected a 3-d tensor [batch, q_heads, head_dim]")
+        shape = (table.batch, q.shape[1], self.head_dim)
+        ldq, ldo = _rows("q", q, q.dtype, shape, index), _rows("o", o, q.dtype, shape, index)
+        if table.batch == 0:
+            return
+        s = _stream_handle(torch, stream, index)
+        ws, nbytes = _workspace(torch, workspace, self.workspace_size(q.shape[1], pages) if workspace is None else 0,
+                                index, stream)
+        st = gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(), ldo, q.shape[1], fmt, ws,
+                                       nbytes, s)
+        if st != OK:
+            raise GemmEpiError("gemm_epi_attention_decode", st)
 
 
 # ---- measurement helpers (include/gemm_epi_probes.h) -------------------------

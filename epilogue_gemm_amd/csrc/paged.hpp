@@ -1,0 +1,62 @@
+// paged.hpp -- arithmetic of the paged key-value cache that the append and
+// the decode attention share: lengths, pages and the split of a batch's keys
+// into pieces.  Plain functions of integers, for device and host alike (the
+// CPU tests compile them with a host compiler and check every bound).
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define GE_HD __host__ __device__ __forceinline__
+#else
+#define GE_HD inline
+#endif
+
+namespace ge {
+namespace paged {
+
+constexpr int kUnit = 128;  // keys are split in units of this many (4 waves x 32)
+
+// Tokens of a sequence: its stored length clamped to what its row of the
+// page table can hold (cap = width * page_size < 2^31).
+GE_HD int seq_len(int stored, int cap) { return stored < 0 ? 0 : stored < cap ? stored : cap; }
+
+// A page table entry that names a page of the cache, else -1.
+GE_HD int page_or_none(int entry, int num_pages) { return entry >= 0 && entry < num_pages ? entry : -1; }
+
+// Row number of (page, head, slot) in a [num_pages, heads, page_size] array.
+GE_HD int64_t row_of(int page, int heads, int head, int page_size, int slot) {
+  return ((int64_t)page * heads + head) * page_size + slot;
+}
+
+// Where the new token `row` of a sequence whose rows end before `end` goes:
+// its position, or -1 when that is outside the sequence or the table.
+GE_HD int new_position(int stored_len, int end, int row, int cap) {
+  const int64_t p = (int64_t)stored_len - ((int64_t)end - row);
+  return p >= 0 && p < cap ? (int)p : -1;
+}
+
+// Units of a sequence.
+GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
+
+// Units per piece when all sequences' units are cut into about `target`
+// pieces; then the pieces of one sequence (one for an empty sequence too: it
+// writes the zeros).  Over a batch of n sequences, sum(pieces) <= target + n.
+GE_HD int piece_units(int total_units, int target) {
+  return total_units <= target ? 1 : total_units / target + (total_units % target != 0);
+}
+GE_HD int pieces_of(int units, int per_piece) {
+  return units == 0 ? 1 : units / per_piece + (units % per_piece != 0);
+}
+
+// Pieces per (key head, query tile) the decode attention aims at, and the
+// most that a batch can then have (the grid's x extent).
+GE_HD int piece_target(int columns, int workgroups) { return workgroups <= columns ? 1 : workgroups / columns; }
+GE_HD int64_t piece_bound(int64_t batch, int64_t cap, int target) {
+  const int64_t per_seq = cap < kUnit ? 1 : (cap + kUnit - 1) / kUnit;
+  const int64_t all = batch * per_seq, some = (int64_t)target + batch;
+  return all < some ? all : some;
+}
+
+}  // namespace paged
+}  // namespace ge

@@ -1,0 +1,601 @@
+// paged_cache.hip -- the paged key-value cache of a layer: the append of new
+// tokens and the attention of one new token of each sequence over its pages,
+//
+//     O[i, h] = sum_j softmax_j(q . k_j / sqrt(D)) v_j     j < lens[i], page of j present
+//
+// with the keys of a sequence split over workgroups (pieces) and the pieces
+// joined by a second kernel.
+//
+// A workgroup takes one piece of one sequence, one key head and up to 16 of
+// the query heads that share it; each of its four waves takes every fourth
+// tile of 32 keys.  Both products are v_mfma_f32_16x16x32 chains whose
+// operands come straight from memory and whose layouts meet without any
+// movement between lanes (c = lane % 16, h = lane / 16):
+//   * S^T = K Q^T: first operand 16 keys (lane c: key c, 8 values of it),
+//     second the 16 query heads; lane (c, h) receives, for query head c,
+//     the scores of keys 4 h + 0..3 of each group of 16;
+//   * the probabilities of two groups are then the lane's second operand of
+//     O^T = V^T P^T for 32 keys if the 32 places of the k axis are numbered
+//     (h, u) -> key 16 (u / 4) + 4 h + u % 4;
+//   * V^T's first operand for D / 16 products: lane (c, h) loads those eight
+//     keys' values d = VEC c .. VEC c + VEC - 1 (VEC = D / 16; 16 lanes read
+//     a whole row) and packs pairs of keys by v_perm; product j takes d =
+//     VEC c + j.  Lane (c, h) ends with VEC consecutive values of query head
+//     c's output for each e: d = VEC (4 h + e) + j.
+#include "gemm_tile16.hpp"
+#include "paged.hpp"
+
+#include "../../include/gemm_epi_decode.h"
+
+namespace ge {
+namespace paged {
+
+using tile16::mfma16;
+
+constexpr float kNegInf = -__builtin_inff();
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+  char *k, *v;  // the cache
+  float *ks, *vs;
+  const int32_t *pages, *lens, *starts;
+  const void *K, *V;
+  int64_t ld, ldk, ldv;
+  int num_pages, page_size, heads, width, batch, tokens;
+};
+
+// 2^e, e the smallest integer >= -100 with amax <= 448 * 2^e; NaN for an
+// infinite or NaN amax.  amax = m 2^k, m in [1/2, 1): 448 = 0.875 * 2^9.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  if (!(amax < __builtin_inff())) return __builtin_nanf("");
+  if (amax == 0.0f) return 0x1p-100f;
+  const int k = __builtin_amdgcn_frexp_expf(amax);
+  const int e = k - (__builtin_amdgcn_frexp_mantf(amax) > 0.875f ? 8 : 9);
+  return __builtin_amdgcn_ldexpf(1.0f, max(e, -100));
+}
+
+// One wave a token: its sequence, page and slot, then the rows of all heads,
+// 8 values a lane.  An E4M3 row's largest value is found over the D / 8
+// lanes that hold it.
+template <typename T, bool FP8, int D>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
+  constexpr int LPR = D / 8;  // lanes of a row
+  const int lane = threadIdx.x & 63;
+  const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (t >= a.tokens) return;
+  int seq = t, end = t + 1;
+  if (a.starts) {
+    // the number of sequences whose rows end at or before this one
+    seq = 0;
+    for (int i = 0; i < a.batch; i += 64) {
+      const bool past = i + lane < a.batch && a.starts[i + lane + 1] <= t;
+      seq += __builtin_popcountll(__builtin_amdgcn_ballot_w64(past));
+    }
+    if (seq >= a.batch || a.starts[0] > t) return;
+    end = a.starts[seq + 1];
+  }
+  const int pos = new_position(a.lens[seq], end, t, a.width * a.page_size);
+  if (pos < 0) return;
+  const int page = page_or_none(a.pages[seq * a.ld + pos / a.page_size], a.num_pages);
+  if (page < 0) return;
+  const int64_t row0 = row_of(page, a.heads, 0, a.page_size, pos % a.page_size);
+  const int n = a.heads * LPR;
+  for (int i = lane; i < 2 * n; i += 64) {
+    const bool val = i >= n;
+    const int j = val ? i - n : i, head = j / LPR, at = j % LPR;
+    const T* src = val ? (const T*)a.V + t * a.ldv : (const T*)a.K + t * a.ldk;
+    const u32x4 x = *(const u32x4*)(src + 8 * j);
+    const int64_t row = row0 + (int64_t)head * a.page_size;
+    char* dst = val ? a.v : a.k;
+    if constexpr (!FP8) {
+      *(u32x4*)(dst + (row * D + 8 * at) * 2) = x;
+    } else {
+      float f[8];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[2 * w] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[w] & 0xffffu)));
+        f[2 * w + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[w] >> 16)));
+      }
+      // by the bits of |x|, which order a NaN above every number
+      uint32_t mx = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mx = max(mx, __builtin_bit_cast(uint32_t, f[u]) & 0x7fffffffu);
+#pragma unroll
+      for (int m = 1; m < LPR; m <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, m));
+      const float s = pow2_scale(__builtin_bit_cast(float, mx));
+      const float inv = 1.0f / s;
+      u32x2 q;
+      q.x = pack4_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+      q.y = pack4_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+      *(u32x2*)(dst + row * D + 8 * at) = q;
+      if (at == 0) (val ? a.vs : a.ks)[row] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// decode attention
+// ---------------------------------------------------------------------------
+struct DecodeArgs {
+  const char *k, *v;
+  const float *ks, *vs;
+  const int32_t *pages, *lens;
+  const void* Q;
+  void* O;
+  float* part;  // per (piece, column): 16 x D sums, then 16 x (maximum, sum)
+  int64_t ld, ldq, ldo;
+  int num_pages, page_size, heads, width, batch;
+  int group;   // query heads per key head
+  int qtiles;  // tiles of 16 of them
+  int target;  // pieces aimed at
+  float scale_log2;
+};
+
+__device__ __forceinline__ int wave_sum(int v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// The split of the batch's keys into pieces, found by each wave for itself:
+// lane l counts for sequences l * per .. + per - 1.
+struct Split {
+  int per, i0, i1;  // this lane's sequences
+  int unit;         // units per piece
+  int own, before;  // pieces of this lane's sequences, and of those before them
+};
+__device__ __forceinline__ Split split_batch(const int32_t* lens, int batch, int cap, int target, int lane) {
+  Split s;
+  s.per = (batch + 63) / 64;
+  s.i0 = min(lane * s.per, batch);
+  s.i1 = min(s.i0 + s.per, batch);
+  int units = 0;
+  for (int i = s.i0; i < s.i1; ++i) units += units_of(seq_len(lens[i], cap));
+  s.unit = piece_units(wave_sum(units), target);
+  s.own = 0;
+  for (int i = s.i0; i < s.i1; ++i) s.own += pieces_of(units_of(seq_len(lens[i], cap)), s.unit);
+  int incl = s.own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(incl, d);
+    if (lane >= d) incl += up;
+  }
+  s.before = incl - s.own;
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ float* part_of(const DecodeArgs& a, int piece, int column, int columns) {
+  return a.part + ((int64_t)piece * columns + column) * (16 * (D + 2));
+}
+
+// 8-bit codes 2 HI and 2 HI + 1 of src as two 16-bit values, times the
+// power of two `scale`
+template <typename T, bool HI>
+__device__ __forceinline__ uint32_t widen2(uint32_t src, float scale) {
+  if constexpr (__is_same(T, f16))
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(src, scale, HI));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, scale, HI));
+}
+
+template <typename T, bool FP8, int D>
+__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
+  constexpr int VEC = D / 16;                // values of a row per lane in V's operand
+  constexpr int KS = D / 32;                 // 32-deep steps of a score
+  constexpr int EB = FP8 ? 1 : 2;            // bytes of a cache element
+  constexpr int KL = D * EB / 64;            // 16-byte loads of a lane for its key
+  constexpr int VW = VEC * EB / 4;           // 32-bit words of a lane for one key's V
+  __shared__ float sm[4][16], sl[4][16], so[4][16][D + 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, h = lane >> 4;
+  const int cap = a.width * a.page_size;
+
+  // the piece: the lane whose sequences hold piece blockIdx.x walks to it
+  const Split sp = split_batch(a.lens, a.batch, cap, a.target, lane);
+  const int piece = blockIdx.x;
+  const uint64_t owner = __builtin_amdgcn_ballot_w64(piece >= sp.before && piece < sp.before + sp.own);
+  if (owner == 0) return;
+  int seq = sp.i0, at = sp.before, count = 0;
+  for (int i = sp.i0; i < sp.i1; ++i) {
+    const int n = pieces_of(units_of(seq_len(a.lens[i], cap)), sp.unit);
+    if (piece < at + n) {
+      seq = i;
+      count = n;
+      break;
+    }
+    at += n;
+  }
+  const int src = __builtin_ctzll(owner);
+  seq = __builtin_amdgcn_readlane(seq, src);
+  count = __builtin_amdgcn_readlane(count, src);
+  const int index = piece - __builtin_amdgcn_readlane(at, src);
+  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lens[seq], cap));
+  // (units up to the cap fit an int; the last piece's end need not)
+  const int kbeg = index * sp.unit * kUnit;
+  const int kend = (int)min((int64_t)len, (int64_t)(index + 1) * sp.unit * kUnit);
+
+  // the query heads of this column
+  const int columns = a.heads * a.qtiles;
+  const int head = blockIdx.y / a.qtiles, first = (blockIdx.y % a.qtiles) * 16;
+  const bool query = first + c < a.group;
+  const T* q = (const T*)a.Q + seq * a.ldq + (int64_t)(head * a.group + first + c) * D;
+  u32x4 qf[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    // the 8 values of a row that lane (., h) multiplies in step s
+    const int d = FP8 ? 64 * (s >> 1) + 16 * h + 8 * (s & 1) : 32 * s + 8 * h;
+    qf[s] = query ? *(const u32x4*)(q + d) : u32x4{};
+  }
+
+  f32x4 acc[VEC] = {};
+  float m = kNegInf, l = 0.0f;
+  for (int k0 = kbeg + 32 * wave; k0 < kend; k0 += 128) {
+    int64_t row[2];
+    int valid[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int gk = k0 + 16 * g;
+      const int page = gk < kend ? page_or_none(a.pages[seq * a.ld + gk / a.page_size], a.num_pages) : -1;
+      valid[g] = page < 0 ? 0 : min(kend - gk, 16);
+      row[g] = row_of(max(page, 0), a.heads, head, a.page_size, gk % a.page_size);
+    }
+    // scores
+    f32x4 s[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const char* kr = a.k + (row[g] + c) * (D * EB) + 16 * h;
+      s[g] = f32x4{};
+      if constexpr (FP8) {
+        const float scale = a.ks[row[g] + c];
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+          const u32x4 x = *(const u32x4*)(kr + 64 * i);
+          const u32x4 lo = {widen2<T, false>(x[0], scale), widen2<T, true>(x[0], scale),
+                            widen2<T, false>(x[1], scale), widen2<T, true>(x[1], scale)};
+          const u32x4 hi = {widen2<T, false>(x[2], scale), widen2<T, true>(x[2], scale),
+                            widen2<T, false>(x[3], scale), widen2<T, true>(x[3], scale)};
+          s[g] = mfma16<T>(lo, qf[2 * i], s[g]);
+          s[g] = mfma16<T>(hi, qf[2 * i + 1], s[g]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(*(const u32x4*)(kr + 64 * i), qf[i], s[g]);
+      }
+      s[g] *= a.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * h + e >= valid[g]) s[g][e] = kNegInf;
+    }
+    // running maximum of the query head over all four quarters
+    float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                     fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float mn = fmaxf(m, mx);
+    const float ref = mn == kNegInf ? 0.0f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
+    // probabilities, in two parts
+    u32x4 ph, pl;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float p0 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1)] - ref);
+      const float p1 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1) + 1] - ref);
+      l += p0 + p1;
+      const T t0 = from_f32<T>(p0), t1 = from_f32<T>(p1);
+      ph[w] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
+      pl[w] = pack2_out<T>(p0 - to_f32(t0), p1 - to_f32(t1));
+    }
+    // V: this lane's eight keys
+    uint32_t vr[8][VEC / 2];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int g = u >> 2, key = 4 * h + (u & 3);
+      const char* vp = a.v + (row[g] + key) * (D * EB) + c * (VEC * EB);
+      uint32_t x[VW];
+      if constexpr (VW == 4) {
+        const u32x4 y = *(const u32x4*)vp;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) x[w] = y[w];
+      } else if constexpr (VW == 2) {
+        const u32x2 y = *(const u32x2*)vp;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) x[w] = y[w];
+      } else {
+        x[0] = *(const uint32_t*)vp;
+      }
+      // a key without a page or past the end: its V may hold anything, and
+      // zero times anything need not be zero
+      const bool in = key < valid[g];
+      if constexpr (FP8) {
+        const float scale = a.vs[row[g] + key];
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          vr[u][2 * w] = in ? widen2<T, false>(x[w], scale) : 0u;
+          vr[u][2 * w + 1] = in ? widen2<T, true>(x[w], scale) : 0u;
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) vr[u][w] = in ? x[w] : 0u;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      u32x4 vf;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][j >> 1], vr[2 * w][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+      acc[j] = mfma16<T>(vf, ph, acc[j]);
+      acc[j] = mfma16<T>(vf, pl, acc[j]);
+    }
+  }
+
+  // join the four waves
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (h == 0) {
+    sm[wave][c] = m;
+    sl[wave][c] = l;
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) so[wave][c][VEC * (4 * h + e) + j] = acc[j][e];
+  __syncthreads();
+  const int qh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * VEC;
+  if (first + qh >= a.group) return;
+  const float mj = fmaxf(fmaxf(sm[0][qh], sm[1][qh]), fmaxf(sm[2][qh], sm[3][qh]));
+  const float ref = mj == kNegInf ? 0.0f : mj;
+  float o[VEC] = {}, lj = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = __builtin_amdgcn_exp2f(sm[w][qh] - ref);
+    lj += f * sl[w][qh];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] += f * so[w][qh][d0 + j];
+  }
+  if (count == 1) {
+    const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
+    T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
+  } else {
+    float* pp = part_of<D>(a, piece, blockIdx.y, columns);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) pp[qh * D + d0 + j] = o[j];
+    if (d0 == 0) {
+      pp[16 * D + 2 * qh] = mj;
+      pp[16 * D + 2 * qh + 1] = lj;
+    }
+  }
+}
+
+// Joins the pieces of one sequence and column, in their order.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
+  constexpr int VEC = D / 16;
+  const int lane = threadIdx.x & 63;
+  const int cap = a.width * a.page_size, seq = blockIdx.x;
+  const Split sp = split_batch(a.lens, a.batch, cap, a.target, lane);
+  const int count = pieces_of(units_of(seq_len(a.lens[seq], cap)), sp.unit);
+  if (count == 1) return;
+  int at = sp.before;
+  for (int i = sp.i0; i < sp.i1 && i < seq; ++i) at += pieces_of(units_of(seq_len(a.lens[i], cap)), sp.unit);
+  const int piece = __builtin_amdgcn_readlane(at, seq / sp.per);
+  const int columns = a.heads * a.qtiles;
+  const int head = blockIdx.y / a.qtiles, first = (blockIdx.y % a.qtiles) * 16;
+  const int qh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * VEC;
+  if (first + qh >= a.group) return;
+  float m = kNegInf;
+  for (int p = 0; p < count; ++p) m = fmaxf(m, part_of<D>(a, piece + p, blockIdx.y, columns)[16 * D + 2 * qh]);
+  const float ref = m == kNegInf ? 0.0f : m;
+  float o[VEC] = {}, l = 0.0f;
+  for (int p = 0; p < count; ++p) {
+    const float* pp = part_of<D>(a, piece + p, blockIdx.y, columns);
+    const float f = __builtin_amdgcn_exp2f(pp[16 * D + 2 * qh] - ref);
+    l += f * pp[16 * D + 2 * qh + 1];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] += f * pp[qh * D + d0 + j];
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
+#pragma unroll
+  for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
+}
+
+constexpr int kWorkgroups = 1024;  // aimed at: four for each of the 256 CUs
+
+template <typename T, bool FP8, int D>
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream) {
+  const int columns = a.heads * a.qtiles;
+  const int64_t pieces = piece_bound(a.batch, (int64_t)a.width * a.page_size, a.target);
+  hipLaunchKernelGGL((decode_kernel<T, FP8, D>), dim3((unsigned)pieces, columns), dim3(256), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pieces == a.batch) return e;
+  hipLaunchKernelGGL((join_kernel<T, D>), dim3(a.batch, columns), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool FP8>
+hipError_t launch_append(const AppendArgs& a, int head_dim, hipStream_t stream) {
+  const dim3 grid((a.tokens + 3) / 4), block(256);
+  if (head_dim == 64) hipLaunchKernelGGL((append_kernel<T, FP8, 64>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((append_kernel<T, FP8, 128>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// argument checks
+// ---------------------------------------------------------------------------
+constexpr int64_t kLim = (int64_t)1 << 31;
+
+gemm_epi_status check_cache(const gemm_epi_paged_cache* c, bool pointers) {
+  if (!c || c->num_pages <= 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0) return GEMM_EPI_ERR_INVALID_ARG;
+  if (c->dtype != GEMM_EPI_F16 && c->dtype != GEMM_EPI_BF16 && c->dtype != GEMM_EPI_FP8_E4M3)
+    return GEMM_EPI_ERR_INVALID_ARG;
+  if (pointers) {
+    const bool fp8 = c->dtype == GEMM_EPI_FP8_E4M3;
+    if (!c->k || !c->v || fp8 != (c->k_scale != nullptr) || fp8 != (c->v_scale != nullptr))
+      return GEMM_EPI_ERR_INVALID_ARG;
+  }
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->page_size % 16 != 0 || c->page_size > 65536 || c->heads > 1024 ||
+      c->num_pages >= kLim || c->num_pages * c->page_size >= kLim)
+    return GEMM_EPI_ERR_UNSUPPORTED;
+  if (pointers && (((uintptr_t)c->k | (uintptr_t)c->v | (uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 15u))
+    return GEMM_EPI_ERR_UNSUPPORTED;
+  return GEMM_EPI_OK;
+}
+
+gemm_epi_status check_sizes(int64_t page_size, int64_t batch, int64_t width) {
+  if (batch < 0 || width <= 0) return GEMM_EPI_ERR_INVALID_ARG;
+  // (positions and counts of units are 32-bit integers in the kernels)
+  if (batch > 65535 || width >= kLim || width * page_size > kLim - 256 ||
+      batch * ((width * page_size + kUnit - 1) / kUnit) >= kLim)
+    return GEMM_EPI_ERR_UNSUPPORTED;
+  return GEMM_EPI_OK;
+}
+
+gemm_epi_status check_table(const gemm_epi_paged_cache* c, const gemm_epi_page_table* t) {
+  if (!t || t->ld < t->width) return GEMM_EPI_ERR_INVALID_ARG;
+  const gemm_epi_status s = check_sizes(c->page_size, t->batch, t->width);
+  if (s != GEMM_EPI_OK) return s;
+  if (t->ld >= kLim) return GEMM_EPI_ERR_UNSUPPORTED;
+  if (t->batch > 0 && (!t->pages || !t->lens || (((uintptr_t)t->pages | (uintptr_t)t->lens) & 3u)))
+    return GEMM_EPI_ERR_INVALID_ARG;
+  return GEMM_EPI_OK;
+}
+
+bool formats_fit(const gemm_epi_paged_cache* c, gemm_epi_dtype dtype) {
+  return (dtype == GEMM_EPI_F16 || dtype == GEMM_EPI_BF16) && (c->dtype == dtype || c->dtype == GEMM_EPI_FP8_E4M3);
+}
+
+struct Shape {
+  int group, qtiles, target;
+  int64_t pieces;
+};
+Shape shape_of(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
+  Shape s;
+  s.group = (int)(q_heads / c->heads);
+  s.qtiles = (s.group + 15) / 16;
+  s.target = piece_target((int)c->heads * s.qtiles, kWorkgroups);
+  s.pieces = piece_bound(batch, width * c->page_size, s.target);
+  return s;
+}
+size_t workspace_bytes(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
+  const Shape s = shape_of(c, batch, width, q_heads);
+  return (size_t)s.pieces * (size_t)(c->heads * s.qtiles) * (size_t)(16 * (c->head_dim + 2)) * 4;
+}
+
+template <typename T, bool FP8>
+hipError_t launch_decode(const DecodeArgs& a, int head_dim, hipStream_t stream) {
+  return head_dim == 64 ? launch_decode<T, FP8, 64>(a, stream) : launch_decode<T, FP8, 128>(a, stream);
+}
+
+}  // namespace paged
+}  // namespace ge
+
+extern "C" {
+
+gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const gemm_epi_page_table* table,
+                                      const void* K, int64_t ldk, const void* V, int64_t ldv, const int32_t* starts,
+                                      int64_t tokens, gemm_epi_dtype dtype, void* stream) {
+  using namespace ge::paged;
+  gemm_epi_status s = check_cache(cache, true);
+  if (s == GEMM_EPI_OK) s = check_table(cache, table);
+  if (s != GEMM_EPI_OK) return s;
+  const int64_t row = cache->heads * cache->head_dim;
+  if (!formats_fit(cache, dtype) || tokens < 0 || ldk < row || ldv < row || ((uintptr_t)starts & 3u) ||
+      (!starts && tokens != table->batch))
+    return GEMM_EPI_ERR_INVALID_ARG;
+  if (tokens >= (int64_t)1 << 26 || ldk % 8 != 0 || ldv % 8 != 0) return GEMM_EPI_ERR_UNSUPPORTED;
+  if (tokens == 0 || table->batch == 0) return GEMM_EPI_OK;
+  if (!K || !V) return GEMM_EPI_ERR_INVALID_ARG;
+  if (((uintptr_t)K | (uintptr_t)V) & 15u) return GEMM_EPI_ERR_UNSUPPORTED;
+  const AppendArgs a{(char*)cache->k, (char*)cache->v, cache->k_scale, cache->v_scale,
+                     table->pages,    table->lens,     starts,         K,
+                     V,               table->ld,       ldk,            ldv,
+                     (int)cache->num_pages, (int)cache->page_size, (int)cache->heads, (int)table->width,
+                     (int)table->batch, (int)tokens};
+  const hipStream_t st = (hipStream_t)stream;
+  const int d = (int)cache->head_dim;
+  const bool fp8 = cache->dtype == GEMM_EPI_FP8_E4M3;
+  const hipError_t e =
+      dtype == GEMM_EPI_F16
+          ? (fp8 ? launch_append<ge::f16, true>(a, d, st) : launch_append<ge::f16, false>(a, d, st))
+          : (fp8 ? launch_append<ge::bf16, true>(a, d, st) : launch_append<ge::bf16, false>(a, d, st));
+  if (e != hipSuccess) {
+    ge::set_last_hip_error((int)e);
+    return GEMM_EPI_ERR_HIP;
+  }
+  return GEMM_EPI_OK;
+}
+
+size_t gemm_epi_attention_decode_workspace_size(const gemm_epi_paged_cache* cache, int64_t batch, int64_t width,
+                                                int64_t q_heads) {
+  using namespace ge::paged;
+  if (check_cache(cache, false) != GEMM_EPI_OK || check_sizes(cache->page_size, batch, width) != GEMM_EPI_OK ||
+      q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 16384 || batch == 0)
+    return 0;
+  return workspace_bytes(cache, batch, width, q_heads);
+}
+
+gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, const gemm_epi_page_table* table,
+                                          const void* Q, int64_t ldq, void* O, int64_t ldo, int64_t q_heads,
+                                          gemm_epi_dtype dtype, void* workspace, size_t workspace_bytes_given,
+                                          void* stream) {
+  using namespace ge::paged;
+  gemm_epi_status s = check_cache(cache, true);
+  if (s == GEMM_EPI_OK) s = check_table(cache, table);
+  if (s != GEMM_EPI_OK) return s;
+  if (!formats_fit(cache, dtype) || q_heads <= 0 || q_heads % cache->heads != 0) return GEMM_EPI_ERR_INVALID_ARG;
+  if (q_heads > 16384) return GEMM_EPI_ERR_UNSUPPORTED;
+  const int64_t row = q_heads * cache->head_dim;
+  if (ldq < row || ldo < row) return GEMM_EPI_ERR_INVALID_ARG;
+  if (ldq % 8 != 0 || ldo % 8 != 0) return GEMM_EPI_ERR_UNSUPPORTED;
+  if (table->batch == 0) return GEMM_EPI_OK;
+  if (!Q || !O || !workspace || workspace_bytes_given < workspace_bytes(cache, table->batch, table->width, q_heads))
+    return GEMM_EPI_ERR_INVALID_ARG;
+  if (((uintptr_t)Q | (uintptr_t)O | (uintptr_t)workspace) & 15u) return GEMM_EPI_ERR_UNSUPPORTED;
+  const Shape sh = shape_of(cache, table->batch, table->width, q_heads);
+  const int d = (int)cache->head_dim;
+  const DecodeArgs a{(const char*)cache->k,
+                     (const char*)cache->v,
+                     cache->k_scale,
+                     cache->v_scale,
+                     table->pages,
+                     table->lens,
+                     Q,
+                     O,
+                     (float*)workspace,
+                     table->ld,
+                     ldq,
+                     ldo,
+                     (int)cache->num_pages,
+                     (int)cache->page_size,
+                     (int)cache->heads,
+                     (int)table->width,
+                     (int)table->batch,
+                     sh.group,
+                     sh.qtiles,
+                     sh.target,
+                     (float)(1.4426950408889634 / __builtin_sqrt((double)d))};
+  const hipStream_t st = (hipStream_t)stream;
+  const bool fp8 = cache->dtype == GEMM_EPI_FP8_E4M3;
+  const hipError_t e =
+      dtype == GEMM_EPI_F16
+          ? (fp8 ? launch_decode<ge::f16, true>(a, d, st) : launch_decode<ge::f16, false>(a, d, st))
+          : (fp8 ? launch_decode<ge::bf16, true>(a, d, st) : launch_decode<ge::bf16, false>(a, d, st));
+  if (e != hipSuccess) {
+    ge::set_last_hip_error((int)e);
+    return GEMM_EPI_ERR_HIP;
+  }
+  return GEMM_EPI_OK;
+}
+
+}  // extern "C"
