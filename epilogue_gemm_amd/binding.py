@@ -299,68 +299,85 @@ def gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads) -> in
     return int(load_library().gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads))
 
 
-def _device_check(name, t, index):
+# What the tensor calls below check is cheap to compare and slow to explain:
+# they compare inline and come here only to say what was wrong.
+
+def _explain(name, t, dtype, shape, index, strided):
+    """Raises the ValueError that fits a tensor which is not a CUDA tensor of
+    this dtype and shape on device `index`, packed but for the first axis
+    where `strided`."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
     if t.get_device() != index:
         raise ValueError(f"{name}: on device {t.get_device()}, the current device is {index}")
-
-
-def _rows(name, t, dtype, shape, index):
-    """Checks a tensor whose first axis may be strided and whose other axes
-    are packed, and returns the elements between its rows."""
-    _device_check(name, t, index)
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    width = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if shape[i] != 1 and st[i] != width:
-            raise ValueError(f"{name}: only the first axis may be strided")
-        width *= shape[i]
-    return st[0] if shape[0] > 1 else width  # one row has no distance to a next one
+    raise ValueError(f"{name}: only the first axis may be strided" if strided else f"{name}: expected a contiguous tensor")
+
+
+def _rows2(name, t, dtype, shape, index):
+    """Elements between the rows of a 2-d tensor with packed columns."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _explain(name, t, dtype, shape, index, True)
+    ld, one = t.stride()
+    if one != 1 and shape[1] != 1:
+        _explain(name, t, dtype, shape, index, True)
+    return ld if shape[0] != 1 else shape[1]  # one row has no distance to a next one
+
+
+def _rows3(name, t, dtype, shape, index):
+    """Elements between the rows of a 3-d tensor with packed rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _explain(name, t, dtype, shape, index, True)
+    ld, mid, one = t.stride()
+    if (one != 1 and shape[2] != 1) or (mid != shape[2] and shape[1] != 1):
+        _explain(name, t, dtype, shape, index, True)
+    return ld if shape[0] != 1 else shape[1] * shape[2]
 
 
 def _packed(name, t, dtype, shape, index):
-    _device_check(name, t, index)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}")
+    """Address of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _explain(name, t, dtype, shape, index, False)
     return t.data_ptr()
 
 
-def _format(name, t):
+def _half_format(name, t):
+    """Format code of a 16-bit tensor."""
     n = _dtype_name(t)
-    if n not in ("f16", "bf16"):
+    if n != "bf16" and n != "f16":
         raise ValueError(f"{name}: dtype {t.dtype}; expected float16 or bfloat16")
-    return n
+    return DTYPES[n]
 
 
-def _stream_handle(torch, stream, index):
-    """hipStream_t of `stream` (of the current device), or of torch's current
-    stream."""
+def _device_and_stream(torch, stream):
+    """(current device, hipStream_t of `stream` or of torch's current stream)."""
     if stream is None:
-        return _current_stream_handle(torch)
+        get, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if get is not None and raw is not None and torch.cuda.is_initialized():
+            index = get()
+            return index, raw(index)
+        return torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+    index = torch.cuda.current_device()
     if stream.device.index != index:
         raise ValueError(f"stream: on device {stream.device.index}, the current device is {index}")
-    return stream.cuda_stream
+    return index, stream.cuda_stream
 
 
 def _workspace(torch, workspace, need, index, stream):
-    """(pointer, bytes) of the caller's workspace, or of one from torch's
-    allocator on the stream of the call."""
+    """(pointer, bytes) of the caller's workspace, or of one of `need()` bytes
+    from torch's allocator on the stream of the call."""
     if workspace is None:
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+            workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
         else:
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
-    else:
-        _device_check("workspace", workspace, index)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous CUDA tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+                workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {index}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e-6, stream=None):
@@ -372,28 +389,27 @@ def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e
     torch's current stream (or `stream`), not synchronised."""
     import torch
 
-    index = torch.cuda.current_device()
-    if x.dim() != 2:
+    index, s = _device_and_stream(torch, stream)
+    shape, dt = x.shape, x.dtype
+    if len(shape) != 2:
         raise ValueError("x: expected a 2-d tensor [rows, cols]")
-    fmt, shape, dt = _format("x", x), x.shape, x.dtype
+    fmt = out = _half_format("x", x)
     rows, cols = shape
-    ldx = _rows("x", x, dt, shape, index)
-    w = _packed("weight", weight, dt, (cols,), index)
-    r = h = s = None
+    ldx, w = _rows2("x", x, dt, shape, index), _packed("weight", weight, dt, (cols,), index)
+    r = h = sc = None
     ldr = ldh = 0
     if residual is not None:
-        ldr = _rows("residual", residual, dt, shape, index)
-        r = residual.data_ptr()
+        ldr, r = _rows2("residual", residual, dt, shape, index), residual.data_ptr()
     if residual_out is not None:
-        ldh = _rows("residual_out", residual_out, dt, shape, index)
-        h = residual_out.data_ptr()
-    out = fmt
+        ldh, h = _rows2("residual_out", residual_out, dt, shape, index), residual_out.data_ptr()
     if y_scale is not None:
-        out = "fp8"
-        s = _packed("y_scale", y_scale, torch.float32, (rows,), index)
-    ldy = _rows("y", y, torch.float8_e4m3fn if y_scale is not None else dt, shape, index)
-    st = gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, s, rows, cols, eps, fmt, out,
-                          _stream_handle(torch, stream, index)) if rows else OK
+        out, dt = DTYPES["fp8"], torch.float8_e4m3fn
+        sc = _packed("y_scale", y_scale, torch.float32, (rows,), index)
+    ldy = _rows2("y", y, dt, shape, index)
+    if rows == 0:
+        return
+    st = (_lib or load_library()).gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, sc, rows,
+                                                   cols, eps, fmt, out, s)
     if st != OK:
         raise GemmEpiError("gemm_epi_rmsnorm", st)
 
@@ -414,30 +430,28 @@ def lora(x, a, b, ids, c, scale=None, residual=None, workspace=None, stream=None
     projection takes as its residual."""
     import torch
 
-    index = torch.cuda.current_device()
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+    index, s = _device_and_stream(torch, stream)
+    xs, sa, sb, dt = x.shape, a.shape, b.shape, x.dtype
+    if len(xs) != 2 or len(sa) != 3 or len(sb) != 3:
         raise ValueError("x, a, b: expected tensors [M, K], [adapters, rank, K] and [adapters, N, rank]")
-    fmt, dt = _format("x", x), x.dtype
-    M, K = x.shape
-    adapters, rank = a.shape[:2]
-    N = b.shape[1]
-    ldx = _rows("x", x, dt, (M, K), index)
-    pa = _packed("a", a, dt, (adapters, rank, K), index)
-    pb = _packed("b", b, dt, (adapters, N, rank), index)
+    fmt = _half_format("x", x)
+    (M, K), (adapters, rank), N = xs, sa[:2], sb[1]
+    cs = (M, N)
+    ldx = _rows2("x", x, dt, xs, index)
+    pa, pb = _packed("a", a, dt, (adapters, rank, K), index), _packed("b", b, dt, (adapters, N, rank), index)
     pi = _packed("ids", ids, torch.int32, (M,), index)
-    ldc = _rows("c", c, dt, (M, N), index)
+    ldc = _rows2("c", c, dt, cs, index)
     ps = None if scale is None else _packed("scale", scale, torch.float32, (adapters,), index)
     pr, ldr = None, 0
     if residual is not None:
-        ldr = _rows("residual", residual, dt, (M, N), index)
-        pr = residual.data_ptr()
+        ldr, pr = _rows2("residual", residual, dt, cs, index), residual.data_ptr()
     if M == 0:
         return
-    s = _stream_handle(torch, stream, index)
-    ws, nbytes = _workspace(torch, workspace, gemm_epi_lora_workspace_size(M, N, K, rank, adapters)
-                            if workspace is None else 0, index, stream)
-    st = gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
-                       ws, nbytes, s)
+    lib = _lib or load_library()
+    ws, nbytes = _workspace(torch, workspace, lambda: lib.gemm_epi_lora_workspace_size(M, N, K, rank, adapters), index,
+                            stream)
+    st = lib.gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
+                           ws, nbytes, s)
     if st != OK:
         raise GemmEpiError("gemm_epi_lora", st)
 
@@ -456,13 +470,13 @@ class PagedCache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
 
-        if k.dim() != 4:
+        shape = k.shape
+        if len(shape) != 4:
             raise ValueError("k: expected a 4-d tensor [num_pages, heads, page_size, head_dim]")
         fmt = _dtype_name(k)
         if fmt not in ("f16", "bf16", "fp8"):
             raise ValueError(f"k: dtype {k.dtype}; expected float16, bfloat16 or float8_e4m3fn")
         self.device_index = k.get_device()
-        shape = k.shape
         pk = _packed("k", k, k.dtype, shape, self.device_index)
         pv = _packed("v", v, k.dtype, shape, self.device_index)
         if (fmt == "fp8") != (k_scale is not None) or (fmt == "fp8") != (v_scale is not None):
@@ -475,16 +489,16 @@ class PagedCache:
         self.num_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = paged_cache_struct(pk, pv, pks, pvs, shape[0], shape[2], shape[1], shape[3], fmt)
 
-    def _table(self, torch, pages, lens):
-        index = torch.cuda.current_device()
+    def _table(self, torch, pages, lens, index):
         if index != self.device_index:
             raise ValueError(f"the cache is on device {self.device_index}, the current device is {index}")
-        if pages.dim() != 2:
+        shape = pages.shape
+        if len(shape) != 2:
             raise ValueError("pages: expected a 2-d tensor [batch, width]")
-        batch, width = pages.shape
-        ld = _rows("pages", pages, torch.int32, pages.shape, index)
-        return page_table_struct(pages.data_ptr(), ld, width, _packed("lens", lens, torch.int32, (batch,), index),
-                                 batch)
+        batch, width = shape
+        i32 = torch.int32
+        return _PageTable(pages.data_ptr(), _rows2("pages", pages, i32, shape, index), width,
+                          _packed("lens", lens, i32, (batch,), index), batch), batch
 
     def append(self, k, v, pages, lens, starts=None, stream=None):
         """Writes the rows k and v [tokens, heads, head_dim] (rows may be
@@ -493,14 +507,15 @@ class PagedCache:
         from starts[batch] on are ignored; None: one row a sequence."""
         import torch
 
-        table = self._table(torch, pages, lens)
-        index = self.device_index
-        fmt = _format("k", k)
-        shape = (k.shape[0], self.heads, self.head_dim)
-        ldk, ldv = _rows("k", k, k.dtype, shape, index), _rows("v", v, k.dtype, shape, index)
-        p = None if starts is None else _packed("starts", starts, torch.int32, (table.batch + 1,), index)
-        st = gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv, p, shape[0], fmt,
-                                   _stream_handle(torch, stream, index))
+        index, s = _device_and_stream(torch, stream)
+        table, batch = self._table(torch, pages, lens, index)
+        fmt, dt = _half_format("k", k), k.dtype
+        tokens = k.shape[0]
+        shape = (tokens, self.heads, self.head_dim)
+        ldk, ldv = _rows3("k", k, dt, shape, index), _rows3("v", v, dt, shape, index)
+        p = None if starts is None else _packed("starts", starts, torch.int32, (batch + 1,), index)
+        st = (_lib or load_library()).gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                                            p, tokens, fmt, s)
         if st != OK:
             raise GemmEpiError("gemm_epi_cache_append", st)
 
@@ -516,20 +531,20 @@ class PagedCache:
         ``workspace_size`` bytes, else one is allocated."""
         import torch
 
-        table = self._table(torch, pages, lens)
-        index = self.device_index
-        fmt = _format("q", q)
-        if q.dim() != 3:
+        index, s = _device_and_stream(torch, stream)
+        table, batch = self._table(torch, pages, lens, index)
+        fmt, dt = _half_format("q", q), q.dtype
+        shape = q.shape
+        if len(shape) != 3:
             raise ValueError("q: expected a 3-d tensor [batch, q_heads, head_dim]")
-        shape = (table.batch, q.shape[1], self.head_dim)
-        ldq, ldo = _rows("q", q, q.dtype, shape, index), _rows("o", o, q.dtype, shape, index)
-        if table.batch == 0:
+        heads = shape[1]
+        shape = (batch, heads, self.head_dim)
+        ldq, ldo = _rows3("q", q, dt, shape, index), _rows3("o", o, dt, shape, index)
+        if batch == 0:
             return
-        s = _stream_handle(torch, stream, index)
-        ws, nbytes = _workspace(torch, workspace, self.workspace_size(q.shape[1], pages) if workspace is None else 0,
-                                index, stream)
-        st = gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(), ldo, q.shape[1], fmt, ws,
-                                       nbytes, s)
+        ws, nbytes = _workspace(torch, workspace, lambda: self.workspace_size(heads, pages), index, stream)
+        st = (_lib or load_library()).gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(),
+                                                                ldo, heads, fmt, ws, nbytes, s)
         if st != OK:
             raise GemmEpiError("gemm_epi_attention_decode", st)
 
