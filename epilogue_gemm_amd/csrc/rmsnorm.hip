@@ -6,8 +6,8 @@
 // row's scale max|y| / 448.  HBM-bound for many rows (x and r read, h and y
 // written, once each), bound by one launch and one reduction's latency for
 // few.
-#include "common.hpp"
 #include "kernels.hpp"
+#include "wave.hpp"
 
 #include "../../include/gemm_epi_decode.h"
 
@@ -23,124 +23,131 @@ struct Args {
   float eps;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Eight consecutive values of a row, the last ones of it perhaps fewer (zeros
+// then).  ANY: rows at any address of an element (a 16-byte access off its
+// alignment is one instruction all the same) and of any length; else whole
+// and aligned.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+template <bool ANY>
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int j, int cols) {
+  if (j >= cols) return u32x4{};
+  if constexpr (!ANY) return *(const u32x4*)(row + j);
+  if (j + 8 <= cols) return *(const u32x4_any*)(row + j);
+  uint32_t v[8];
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+  for (int u = 0; u < 8; ++u) v[u] = j + u < cols ? row[j + u] : 0u;
+  return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
 }
-__device__ __forceinline__ float wave_max(float v) {
+template <typename T>
+__device__ __forceinline__ void widen(u32x4 w, float (&f)[8]) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = to_f32(__builtin_bit_cast(T, (uint16_t)(w[i] & 0xffffu)));
+    f[2 * i + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(w[i] >> 16)));
+  }
+}
+template <typename T, bool ANY>
+__device__ __forceinline__ void store8(T* row, int j, int cols, const float (&f)[8]) {
+  if (j >= cols) return;
+  if (ANY && j + 8 > cols) {
+    for (int u = 0; u < 8; ++u)
+      if (j + u < cols) row[j + u] = from_f32<T>(f[u]);
+    return;
+  }
+  if constexpr (sizeof(T) == 1) {
+    // within +-448 but for the last place of fp32, by the scale: the
+    // conversion rounds that back, no clamp needed
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
+    const u32x2 w = {(uint32_t)lo, (uint32_t)hi};
+    if constexpr (ANY) *(u32x2_any*)(row + j) = w;
+    else *(u32x2*)(row + j) = w;
+  } else {
+    const u32x4 w = {pack2_out<T>(f[0], f[1]), pack2_out<T>(f[2], f[3]), pack2_out<T>(f[4], f[5]), pack2_out<T>(f[6], f[7])};
+    if constexpr (ANY) *(u32x4_any*)(row + j) = w;
+    else *(u32x4*)(row + j) = w;
+  }
 }
 
-// V consecutive values (8, or 1 where rows are not 16-byte aligned) as fp32.
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* p, float (&f)[V]) {
-  if constexpr (V == 8) {
-    const u32x4 w = *(const u32x4*)p;
+// A row in the registers of a workgroup's waves (LPR = 0), or of LPR = 16
+// lanes of one of four waves, each lane VPT pieces of eight values: every tensor is read or written
+// once, each place by one thread, which has read what H or Y may overwrite
+// there before it writes.  All loads, the weights'
+// included, are issued before anything waits, and the sum and an E4M3
+// output's largest |h w| (its scale needs only that times 1 / rms) cross the
+// waves together: one memory latency and one barrier a row.
+template <typename T, typename TOut, bool ANY, int VPT, int LPR>
+__global__ __launch_bounds__(LPR ? 256 : 1024) void rmsnorm_rows(Args a) {
+  constexpr bool FP8 = sizeof(TOut) == 1;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  __shared__ f32x2 part[2][16];  // of alternate rows
+  constexpr int RPB = LPR ? 256 / LPR : 1;  // rows a workgroup
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int at = (LPR ? threadIdx.x % LPR : threadIdx.x) * 8, step = (LPR ? LPR : (int)blockDim.x) * 8;
+  const int64_t row0 = (int64_t)blockIdx.x * RPB + (LPR ? threadIdx.x / LPR : 0);
+  int slot = 0;
+  for (int64_t row = row0; row < a.rows; row += (int64_t)gridDim.x * RPB, slot ^= 1) {
+    const uint16_t* x = (const uint16_t*)a.X + row * a.ldx;
+    const uint16_t* r = a.R ? (const uint16_t*)a.R + row * a.ldr : nullptr;
+    u32x4 xr[VPT], rr[VPT], wr[VPT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = to_f32(__builtin_bit_cast(T, (uint16_t)(w[i] & 0xffffu)));
-      f[2 * i + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(w[i] >> 16)));
+    for (int i = 0; i < VPT; ++i) xr[i] = load8<ANY>(x, at + i * step, a.cols);
+    if (r) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) rr[i] = load8<ANY>(r, at + i * step, a.cols);
     }
-  } else {
-    f[0] = to_f32(p[0]);
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_row(T* p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    p[0] = from_f32<T>(f[0]);
-  } else if constexpr (sizeof(T) == 1) {
-    *(u32x2*)p = u32x2{pack4_e4m3(f[0], f[1], f[2], f[3]), pack4_e4m3(f[4], f[5], f[6], f[7])};
-  } else {
-    *(u32x4*)p = u32x4{pack2_out<T>(f[0], f[1]), pack2_out<T>(f[2], f[3]), pack2_out<T>(f[4], f[5]),
-                       pack2_out<T>(f[6], f[7])};
-  }
-}
-
-// A row in the registers of WPR waves (1 or 4: 256 threads, 4 or 1 rows a
-// workgroup; 16: 1024 threads), each lane VPT pieces of V values: every
-// tensor is read or written once, and H or Y may be X or R, since a row is
-// whole in registers before the reduction that precedes its first store.
-template <typename T, typename TOut, int V, int WPR, int VPT>
-__global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void rmsnorm_rows(Args a) {
-  constexpr int RPB = WPR == 1 ? 4 : 1;
-  __shared__ float part[2][WPR];
-  const int wave = threadIdx.x >> 6;
-  const int at = (WPR == 1 ? (threadIdx.x & 63) : threadIdx.x) * V;
-  constexpr int step = WPR * 64 * V;
-  auto reduce = [&](float v, int slot, bool max_of) {
-    v = max_of ? wave_max(v) : wave_sum(v);
-    if constexpr (WPR > 1) {
-      if ((threadIdx.x & 63) == 0) part[slot][wave] = v;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) wr[i] = load8<ANY>((const uint16_t*)a.W, at + i * step, a.cols);
+    float h[VPT][8];  // h, then h w
+    float ss = 0.0f, mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float f[8];
+      widen<T>(xr[i], h[i]);
+      if (r) {
+        widen<T>(rr[i], f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) h[i][u] += f[u];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ss = __builtin_fmaf(h[i][u], h[i][u], ss);
+      if (a.H) store8<T, ANY>((T*)a.H + row * a.ldh, at + i * step, a.cols, h[i]);
+      widen<T>(wr[i], f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        h[i][u] *= f[u];
+        if constexpr (FP8) mx = fmaxf(mx, fabsf(h[i][u]));
+      }
+    }
+    ss = LPR == 16 ? wave::over_row<wave::Sum>(ss) : wave::all<wave::Sum>(ss);
+    if constexpr (FP8) mx = LPR == 16 ? wave::over_row<wave::Max>(mx) : wave::all<wave::Max>(mx);
+    if constexpr (LPR == 0) {
+      // (a wave that is a row ahead writes the other slot, and none can be
+      // two ahead of a wave still reading)
+      if ((threadIdx.x & 63) == 0) part[slot][wave] = f32x2{ss, mx};
       __syncthreads();
-      v = part[slot][0];
-#pragma unroll
-      for (int i = 1; i < WPR; ++i) v = max_of ? fmaxf(v, part[slot][i]) : v + part[slot][i];
-    }
-    return v;
-  };
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (WPR == 1 ? wave : 0); row < a.rows; row += (int64_t)gridDim.x * RPB) {
-    const T* x = (const T*)a.X + row * a.ldx;
-    float h[VPT][V];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int j = at + i * step;
-#pragma unroll
-      for (int u = 0; u < V; ++u) h[i][u] = 0.0f;
-      if (j < a.cols) load_row<T, V>(x + j, h[i]);
-    }
-    if (a.R) {
-      const T* r = (const T*)a.R + row * a.ldr;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int j = at + i * step;
-        float f[V] = {};
-        if (j < a.cols) load_row<T, V>(r + j, f);
-#pragma unroll
-        for (int u = 0; u < V; ++u) h[i][u] += f[u];
+      ss = 0.0f;
+      for (int i = 0; i < waves; ++i) {
+        ss += part[slot][i].x;
+        if constexpr (FP8) mx = fmaxf(mx, part[slot][i].y);
       }
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int u = 0; u < V; ++u) ss = __builtin_fmaf(h[i][u], h[i][u], ss);
-    ss = reduce(ss, 0, false);
     const float rs = 1.0f / __builtin_sqrtf(ss / (float)a.cols + a.eps);
-    if (a.H) {
-      T* hp = (T*)a.H + row * a.ldh;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (at + i * step < a.cols) store_row<T, V>(hp + at + i * step, h[i]);
-    }
-    float mx = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int j = at + i * step;
-      float w[V] = {};
-      if (j < a.cols) load_row<T, V>((const T*)a.W + j, w);
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-        h[i][u] = h[i][u] * rs * w[u];
-        if (sizeof(TOut) == 1) mx = fmaxf(mx, fabsf(h[i][u]));
-      }
-    }
-    if constexpr (sizeof(TOut) == 1) {
-      const float s = fmaxf(reduce(mx, 1, true) / 448.0f, 0x1p-100f), inv = 1.0f / s;
+    float f = rs;
+    if constexpr (FP8) {
+      const float s = fmaxf(mx * rs / 448.0f, 0x1p-100f);
+      f = rs / s;
       if (at == 0) a.y_scale[row] = s;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int u = 0; u < V; ++u) h[i][u] *= inv;
     }
     TOut* yp = (TOut*)a.Y + row * a.ldy;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (at + i * step < a.cols) store_row<TOut, V>(yp + at + i * step, h[i]);
-    if constexpr (WPR > 1) __syncthreads();  // `part` is free for the next row
+    for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) h[i][u] *= f;
+      store8<TOut, ANY>(yp, at + i * step, a.cols, h[i]);
+    }
   }
 }
 
@@ -164,7 +171,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(Args a) {
       const float h = load(j);
       ss = __builtin_fmaf(h, h, ss);
     }
-    ss = wave_sum(ss);
+    ss = wave::all<wave::Sum>(ss);
     if ((tid & 63) == 0) part[0][tid >> 6] = ss;
     __syncthreads();
     ss = 0.0f;
@@ -174,7 +181,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(Args a) {
     if constexpr (sizeof(TOut) == 1) {
       float mx = 0.0f;
       for (int64_t j = tid; j < a.cols; j += 1024) mx = fmaxf(mx, fabsf(load(j) * rs * to_f32(w[j])));
-      mx = wave_max(mx);
+      mx = wave::all<wave::Max>(mx);
       if ((tid & 63) == 0) part[1][tid >> 6] = mx;
       __syncthreads();
       mx = 0.0f;
@@ -196,36 +203,39 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(Args a) {
 
 constexpr int kMaxGrid = 1 << 20;  // a grid's threads fit 32 bits; further rows by the kernels' loops
 
-template <typename T, typename TOut, int V, int WPR, int VPT>
+template <typename T, typename TOut, bool ANY, int VPT, int LPR>
 hipError_t launch_rows(const Args& a, hipStream_t stream) {
-  const int wgs = WPR == 1 ? (a.rows + 3) / 4 : a.rows;
-  hipLaunchKernelGGL((rmsnorm_rows<T, TOut, V, WPR, VPT>), dim3(min(wgs, kMaxGrid)), dim3(WPR == 16 ? 1024 : 256), 0,
-                     stream, a);
+  constexpr int RPB = LPR ? 256 / (LPR + !LPR) : 1;
+  const int wgs = (int)(((int64_t)a.rows + RPB - 1) / RPB);
+  const int waves = LPR ? 4 : (a.cols + 512 * VPT - 1) / (512 * VPT);
+  hipLaunchKernelGGL((rmsnorm_rows<T, TOut, ANY, VPT, LPR>), dim3(min(wgs, kMaxGrid)), dim3(64 * waves), 0, stream, a);
   return hipGetLastError();
 }
 
-// The fewest waves whose registers hold a row: 8-value pieces where every
-// row of every tensor allows 16-byte accesses, else single values.
-template <typename T, typename TOut>
-hipError_t launch(const Args& a, hipStream_t stream) {
-  const int64_t lds = a.ldx | a.ldy | (a.R ? a.ldr : 0) | (a.H ? a.ldh : 0);
-  const uintptr_t ptrs = (uintptr_t)a.X | (uintptr_t)a.R | (uintptr_t)a.W | (uintptr_t)a.H |
-                         (sizeof(TOut) == 1 ? (uintptr_t)a.Y << 1 : (uintptr_t)a.Y);
-  if (a.cols % 8 == 0 && (lds & 7) == 0 && (ptrs & 15u) == 0) {
-    if (a.cols <= 512) return launch_rows<T, TOut, 8, 1, 1>(a, stream);
-    if (a.cols <= 2048) return launch_rows<T, TOut, 8, 4, 1>(a, stream);
-    if (a.cols <= 4096) return launch_rows<T, TOut, 8, 4, 2>(a, stream);
-    if (a.cols <= 8192) return launch_rows<T, TOut, 8, 4, 4>(a, stream);
-    if (a.cols <= 16384) return launch_rows<T, TOut, 8, 16, 2>(a, stream);
-    if (a.cols <= 32768) return launch_rows<T, TOut, 8, 16, 4>(a, stream);
-  } else {
-    if (a.cols <= 256) return launch_rows<T, TOut, 1, 1, 4>(a, stream);
-    if (a.cols <= 1024) return launch_rows<T, TOut, 1, 4, 4>(a, stream);
-    if (a.cols <= 4096) return launch_rows<T, TOut, 1, 4, 16>(a, stream);
-    if (a.cols <= 16384) return launch_rows<T, TOut, 1, 16, 16>(a, stream);
-  }
+// Pieces per lane.  One, with as many waves as that takes, gives a row the
+// shortest latency (4 rows of 4096 with a residual: 2.5 us, two pieces 3.0)
+// and is as fast for many where a residual doubles the bytes in flight
+// (16384 x 8192 bf16: 181 against 188 us).  Many rows without one want two
+// (8192 x 8192 f16 to E4M3: 44 against 54 us; 8192 x 8192 bf16: 54 against
+// 61).  Longer rows take what their 16 waves need.  Up to 128 columns a row
+// is 16 lanes' (200000 x 128: 38 us, a wave each 57).
+template <typename T, typename TOut, bool ANY>
+hipError_t launch_any(const Args& a, hipStream_t stream) {
+  if (a.cols <= 128) return launch_rows<T, TOut, ANY, 1, 16>(a, stream);
+  if (a.cols <= 512 || (a.cols <= 8192 && (a.R || a.rows < 1024))) return launch_rows<T, TOut, ANY, 1, 0>(a, stream);
+  if (a.cols <= 16384) return launch_rows<T, TOut, ANY, 2, 0>(a, stream);
+  if (a.cols <= 32768) return launch_rows<T, TOut, ANY, 4, 0>(a, stream);
   hipLaunchKernelGGL((rmsnorm_long<T, TOut>), dim3(min(a.rows, kMaxGrid)), dim3(1024), 0, stream, a);
   return hipGetLastError();
+}
+
+template <typename T, typename TOut>
+hipError_t launch(const Args& a, hipStream_t stream) {
+  const int64_t lds = a.cols | a.ldx | a.ldy | (a.R ? a.ldr : 0) | (a.H ? a.ldh : 0);
+  const uintptr_t ptrs = (uintptr_t)a.X | (uintptr_t)a.R | (uintptr_t)a.W | (uintptr_t)a.H |
+                         (sizeof(TOut) == 1 ? (uintptr_t)a.Y << 1 : (uintptr_t)a.Y);
+  const bool aligned = (lds & 7) == 0 && (ptrs & 15u) == 0;
+  return aligned ? launch_any<T, TOut, false>(a, stream) : launch_any<T, TOut, true>(a, stream);
 }
 
 }  // namespace norm
