@@ -24,6 +24,20 @@ GE_HD int seq_len(int stored, int cap) { return stored < 0 ? 0 : stored < cap ? 
 // A page table entry that names a page of the cache, else -1.
 GE_HD int page_or_none(int entry, int num_pages) { return entry >= 0 && entry < num_pages ? entry : -1; }
 
+// n / d for n below 2^27 and d from 1 to 4096 (positions and page sizes in
+// groups of 16), as a product and a shift: m = ceil(2^p / d) with 2^p >= 2^27 d,
+// so that m d exceeds 2^p by less than d and n (m d - 2^p) stays below 2^p.
+struct Divider {
+  uint32_t m;
+  int p;
+};
+GE_HD Divider make_divider(int d) {
+  int p = 27;
+  while (((int64_t)1 << (p - 27)) < d) ++p;
+  return Divider{(uint32_t)((((uint64_t)1 << p) + d - 1) / d), p};
+}
+GE_HD int divide(int n, Divider d) { return (int)(((uint64_t)(uint32_t)n * d.m) >> d.p); }
+
 // Row number of (page, head, slot) in a [num_pages, heads, page_size] array.
 GE_HD int64_t row_of(int page, int heads, int head, int page_size, int slot) {
   return ((int64_t)page * heads + head) * page_size + slot;

@@ -24,6 +24,7 @@
 //     c's output for each e: d = VEC (4 h + e) + j.
 #include "gemm_tile16.hpp"
 #include "paged.hpp"
+#include "wave.hpp"
 
 #include "../../include/gemm_epi_decode.h"
 
@@ -130,6 +131,7 @@ struct DecodeArgs {
   int group;   // query heads per key head
   int qtiles;  // tiles of 16 of them
   int target;  // pieces aimed at
+  Divider groups;  // by the groups of 16 tokens of a page
   float scale_log2;
 };
 
@@ -181,13 +183,28 @@ __device__ __forceinline__ uint32_t widen2(uint32_t src, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, scale, HI));
 }
 
+// A tile of 32 keys as loaded: for each group of 16 its key row of this lane
+// and (u = 4 g + 0..3) the V rows of this lane, and how many of the group's
+// keys exist.
+template <bool FP8, int D>
+struct Tile {
+  static constexpr int VEC = D / 16;        // values of a row per lane in V's operand
+  static constexpr int EB = FP8 ? 1 : 2;    // bytes of a cache element
+  static constexpr int KL = D * EB / 64;    // 16-byte loads of a lane for its key
+  static constexpr int VW = VEC * EB / 4;   // 32-bit words of a lane for one key's V
+  typedef uint32_t vwords __attribute__((ext_vector_type(VW == 1 ? 2 : VW)));  // (one word: in .x)
+  u32x4 k[2][KL];
+  vwords v[8];
+  float ks[2];
+  f32x4 vs[2];
+  int valid[2];
+};
+
 template <typename T, bool FP8, int D>
-__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
-  constexpr int VEC = D / 16;                // values of a row per lane in V's operand
-  constexpr int KS = D / 32;                 // 32-deep steps of a score
-  constexpr int EB = FP8 ? 1 : 2;            // bytes of a cache element
-  constexpr int KL = D * EB / 64;            // 16-byte loads of a lane for its key
-  constexpr int VW = VEC * EB / 4;           // 32-bit words of a lane for one key's V
+__global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
+  using Tl = Tile<FP8, D>;
+  constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW;
+  constexpr int KS = D / 32;  // 32-deep steps of a score
   __shared__ float sm[4][16], sl[4][16], so[4][16][D + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
@@ -212,10 +229,11 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
   seq = __builtin_amdgcn_readlane(seq, src);
   count = __builtin_amdgcn_readlane(count, src);
   const int index = piece - __builtin_amdgcn_readlane(at, src);
+  const int unit = __builtin_amdgcn_readfirstlane(sp.unit);
   const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lens[seq], cap));
   // (units up to the cap fit an int; the last piece's end need not)
-  const int kbeg = index * sp.unit * kUnit;
-  const int kend = (int)min((int64_t)len, (int64_t)(index + 1) * sp.unit * kUnit);
+  const int kbeg = index * unit * kUnit;
+  const int kend = (int)min((int64_t)len, (int64_t)(index + 1) * unit * kUnit);
 
   // the query heads of this column
   const int columns = a.heads * a.qtiles;
@@ -232,55 +250,89 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
 
   f32x4 acc[VEC] = {};
   float m = kNegInf, l = 0.0f;
-  for (int k0 = kbeg + 32 * wave; k0 < kend; k0 += 128) {
-    int64_t row[2];
-    int valid[2];
+  const int32_t* table = a.pages + seq * a.ld;
+  // the table's entries for the two groups of a tile (past the end: the
+  // tile's first, whose keys are then masked)
+  struct Pages {
+    int g[2];
+  };
+  auto pages_of = [&](int k0) __attribute__((always_inline)) {
+    Pages p;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) p.g[g] = table[divide((k0 + 16 * g < kend ? k0 + 16 * g : k0) >> 4, a.groups)];
+    return p;
+  };
+  const uint32_t koff = (uint32_t)(c * D * EB + 16 * h), voff = (uint32_t)(4 * h * D * EB + c * VEC * EB);
+  auto load = [&](Tl& t, int k0, Pages p) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int gk = k0 + 16 * g;
-      const int page = gk < kend ? page_or_none(a.pages[seq * a.ld + gk / a.page_size], a.num_pages) : -1;
-      valid[g] = page < 0 ? 0 : min(kend - gk, 16);
-      row[g] = row_of(max(page, 0), a.heads, head, a.page_size, gk % a.page_size);
+      const int gk = k0 + 16 * g, at = gk < kend ? gk : k0;
+      const int page = page_or_none(p.g[g], a.num_pages);
+      t.valid[g] = page < 0 ? 0 : max(0, min(kend - gk, 16));
+      const int64_t row =
+          row_of(max(page, 0), a.heads, head, a.page_size, at - divide(at >> 4, a.groups) * a.page_size);
+      const char* kp = a.k + row * (D * EB);
+      const char* vp = a.v + row * (D * EB);
+#pragma unroll
+      for (int i = 0; i < KL; ++i) t.k[g][i] = *(const u32x4*)(kp + koff + 64 * i);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const char* r = vp + voff + u * D * EB;
+        if constexpr (VW == 1) t.v[4 * g + u].x = *(const uint32_t*)r;
+        else t.v[4 * g + u] = *(const typename Tl::vwords*)r;
+      }
+      if constexpr (FP8) {
+        t.ks[g] = a.ks[row + c];
+        t.vs[g] = *(const f32x4*)(a.vs + row + 4 * h);
+      }
     }
+  };
+  auto multiply = [&](const Tl& t) __attribute__((always_inline)) {
+    const bool whole = t.valid[0] == 16 && t.valid[1] == 16;
     // scores
     f32x4 s[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const char* kr = a.k + (row[g] + c) * (D * EB) + 16 * h;
       s[g] = f32x4{};
       if constexpr (FP8) {
-        const float scale = a.ks[row[g] + c];
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
-          const u32x4 x = *(const u32x4*)(kr + 64 * i);
-          const u32x4 lo = {widen2<T, false>(x[0], scale), widen2<T, true>(x[0], scale),
-                            widen2<T, false>(x[1], scale), widen2<T, true>(x[1], scale)};
-          const u32x4 hi = {widen2<T, false>(x[2], scale), widen2<T, true>(x[2], scale),
-                            widen2<T, false>(x[3], scale), widen2<T, true>(x[3], scale)};
+          const u32x4 x = t.k[g][i];
+          const float f = t.ks[g];
+          const u32x4 lo = {widen2<T, false>(x[0], f), widen2<T, true>(x[0], f), widen2<T, false>(x[1], f),
+                            widen2<T, true>(x[1], f)};
+          const u32x4 hi = {widen2<T, false>(x[2], f), widen2<T, true>(x[2], f), widen2<T, false>(x[3], f),
+                            widen2<T, true>(x[3], f)};
           s[g] = mfma16<T>(lo, qf[2 * i], s[g]);
           s[g] = mfma16<T>(hi, qf[2 * i + 1], s[g]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(*(const u32x4*)(kr + 64 * i), qf[i], s[g]);
+        for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(t.k[g][i], qf[i], s[g]);
       }
       s[g] *= a.scale_log2;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * h + e >= valid[g]) s[g][e] = kNegInf;
     }
-    // running maximum of the query head over all four quarters
+    if (!whole) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * h + e >= t.valid[g]) s[g][e] = kNegInf;
+    }
+    // running maximum of the query head over all four quarters; the sums are
+    // rescaled only when some head's maximum moves
     float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float mn = fmaxf(m, mx);
-    const float ref = mn == kNegInf ? 0.0f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    m = mn;
-    l *= alpha;
+    mx = wave::over_rows<wave::Max>(mx);
+    if (__builtin_amdgcn_ballot_w64(mx > m)) {
+      const float mn = fmaxf(m, mx);
+      const float alpha = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.0f : mn));
+      m = mn;
+      l *= alpha;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
+      for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
+    }
+    const float ref = m == kNegInf ? 0.0f : m;
     // probabilities, in two parts
     u32x4 ph, pl;
 #pragma unroll
@@ -292,38 +344,31 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
       ph[w] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
       pl[w] = pack2_out<T>(p0 - to_f32(t0), p1 - to_f32(t1));
     }
-    // V: this lane's eight keys
+    // V: this lane's eight keys, 16-bit
     uint32_t vr[8][VEC / 2];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int g = u >> 2, key = 4 * h + (u & 3);
-      const char* vp = a.v + (row[g] + key) * (D * EB) + c * (VEC * EB);
-      uint32_t x[VW];
-      if constexpr (VW == 4) {
-        const u32x4 y = *(const u32x4*)vp;
-#pragma unroll
-        for (int w = 0; w < VW; ++w) x[w] = y[w];
-      } else if constexpr (VW == 2) {
-        const u32x2 y = *(const u32x2*)vp;
-#pragma unroll
-        for (int w = 0; w < VW; ++w) x[w] = y[w];
-      } else {
-        x[0] = *(const uint32_t*)vp;
-      }
-      // a key without a page or past the end: its V may hold anything, and
-      // zero times anything need not be zero
-      const bool in = key < valid[g];
       if constexpr (FP8) {
-        const float scale = a.vs[row[g] + key];
+        const float f = t.vs[u >> 2][u & 3];
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          vr[u][2 * w] = in ? widen2<T, false>(x[w], scale) : 0u;
-          vr[u][2 * w + 1] = in ? widen2<T, true>(x[w], scale) : 0u;
+          vr[u][2 * w] = widen2<T, false>(t.v[u][w], f);
+          vr[u][2 * w + 1] = widen2<T, true>(t.v[u][w], f);
         }
       } else {
 #pragma unroll
-        for (int w = 0; w < VW; ++w) vr[u][w] = in ? x[w] : 0u;
+        for (int w = 0; w < VW; ++w) vr[u][w] = t.v[u][w];
       }
+    }
+    // a key without a page or past the end: its V may hold anything, and zero
+    // times anything need not be zero
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (4 * h + (u & 3) >= t.valid[u >> 2]) {
+#pragma unroll
+          for (int w = 0; w < VEC / 2; ++w) vr[u][w] = 0u;
+        }
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -333,6 +378,26 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
         vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][j >> 1], vr[2 * w][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
       acc[j] = mfma16<T>(vf, ph, acc[j]);
       acc[j] = mfma16<T>(vf, pl, acc[j]);
+    }
+  };
+  // This wave's tiles are 128 keys apart.  The next tile's loads, and the
+  // table entries of the one after it, are in flight while one is
+  // multiplied; past the last tile they read it again (from the cache).
+  const int k1 = kbeg + 32 * wave;
+  if (k1 < kend) {
+    const int last = k1 + (kend - 1 - k1) / 128 * 128;
+    Tl t0, t1;
+    load(t0, k1, pages_of(k1));
+    Pages p = pages_of(min(k1 + 128, last));
+    for (int k0 = k1;; k0 += 256) {
+      load(t1, min(k0 + 128, last), p);
+      p = pages_of(min(k0 + 256, last));
+      multiply(t0);
+      if (k0 + 128 > last) break;
+      load(t0, min(k0 + 256, last), p);
+      p = pages_of(min(k0 + 384, last));
+      multiply(t1);
+      if (k0 + 256 > last) break;
     }
   }
 
@@ -584,6 +649,7 @@ gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, con
                      sh.group,
                      sh.qtiles,
                      sh.target,
+                     make_divider((int)cache->page_size / 16),
                      (float)(1.4426950408889634 / __builtin_sqrt((double)d))};
   const hipStream_t st = (hipStream_t)stream;
   const bool fp8 = cache->dtype == GEMM_EPI_FP8_E4M3;

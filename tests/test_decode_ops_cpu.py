@@ -196,6 +196,7 @@ using namespace ge::paged;
 extern "C" {
 int c_seq_len(int s, int cap) { return seq_len(s, cap); }
 int c_page_or_none(int e, int n) { return page_or_none(e, n); }
+int c_divide(int n, int d) { return divide(n, make_divider(d)); }
 int64_t c_row_of(int p, int hs, int h, int ps, int s) { return row_of(p, hs, h, ps, s); }
 int c_new_position(int len, int end, int row, int cap) { return new_position(len, end, row, cap); }
 int c_units_of(int len) { return units_of(len); }
@@ -231,6 +232,15 @@ def test_lengths_and_pages_outside_the_table(paged):
         assert paged.c_seq_len(stored, 64) == min(max(stored, 0), 64)
     for entry in (INT_MIN, -2, -1, 0, 1, 8, 9, 10, INT_MAX):
         assert paged.c_page_or_none(entry, 9) == (entry if 0 <= entry < 9 else -1)
+
+
+def test_page_of_a_position(paged):
+    rng = np.random.default_rng(0)
+    for d in [*range(1, 200), 255, 256, 257, 1000, 4093, 4095, 4096]:
+        top = (1 << 27) - 1
+        ns = {0, 1, d - 1, d, d + 1, top, top - 1, top // d * d, top // d * d - 1, *rng.integers(0, 1 << 27, 50).tolist()}
+        for n in ns:
+            assert paged.c_divide(n, d) == n // d, (n, d)
 
 
 def test_every_row_of_every_page_is_inside_and_its_own(paged):
