@@ -50,27 +50,20 @@ GE_HD int new_position(int stored_len, int end, int row, int cap) {
   return p >= 0 && p < cap ? (int)p : -1;
 }
 
-// Units of a sequence.
+// Units of a sequence (at most 2^24).
 GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 
-// Units per piece when all sequences' units are cut into about `target`
-// pieces; then the pieces of one sequence (one for an empty sequence too: it
-// writes the zeros).  Over a batch of n sequences, sum(pieces) <= target + n.
-GE_HD int piece_units(int total_units, int target) {
-  return total_units <= target ? 1 : total_units / target + (total_units % target != 0);
-}
-GE_HD int pieces_of(int units, int per_piece) {
-  return units == 0 ? 1 : units / per_piece + (units % per_piece != 0);
-}
-
-// Pieces per (key head, query tile) the decode attention aims at, and the
-// most that a batch can then have (the grid's x extent).
-GE_HD int piece_target(int columns, int workgroups) { return workgroups <= columns ? 1 : workgroups / columns; }
-GE_HD int64_t piece_bound(int64_t batch, int64_t cap, int target) {
-  const int64_t per_seq = cap < kUnit ? 1 : (cap + kUnit - 1) / kUnit;
-  const int64_t all = batch * per_seq, some = (int64_t)target + batch;
-  return all < some ? all : some;
-}
+// The keys of a batch are split evenly over its workgroups: with U the units
+// of all sequences and `columns` the (key head, query tile) pairs, unit u of
+// column c has number f = c U + u, and workgroup w takes numbers
+// share_begin(F, w) to share_begin(F, w + 1) - 1 of F = columns * U.  A
+// sequence's units in one column are then cut into pieces where shares end.
+// No workgroup has an empty share: of more workgroups than units the first F
+// take one each.
+GE_HD int sharers(int64_t F, int workgroups) { return F < workgroups ? (int)F : workgroups; }
+GE_HD int64_t share_begin(int64_t F, int w, int workgroups) { return F * w / workgroups; }
+// The workgroup that has number f.
+GE_HD int share_of(int64_t F, int64_t f, int workgroups) { return (int)(((f + 1) * workgroups - 1) / F); }
 
 }  // namespace paged
 }  // namespace ge

@@ -3,12 +3,13 @@
 //
 //     O[i, h] = sum_j softmax_j(q . k_j / sqrt(D)) v_j     j < lens[i], page of j present
 //
-// with the keys of a sequence split over workgroups (pieces) and the pieces
-// joined by a second kernel.
+// with the keys of all sequences and heads split evenly over the workgroups
+// that the chip holds at once (paged.hpp), and the pieces of a sequence that
+// the split cuts joined by a second kernel.
 //
-// A workgroup takes one piece of one sequence, one key head and up to 16 of
-// the query heads that share it; each of its four waves takes every fourth
-// tile of 32 keys.  Both products are v_mfma_f32_16x16x32 chains whose
+// For each piece -- some keys of one sequence, one key head and up to 16 of
+// the query heads that share it -- the four waves of a workgroup take every
+// fourth tile of 32 keys.  Both products are v_mfma_f32_16x16x32 chains whose
 // operands come straight from memory and whose layouts meet without any
 // movement between lanes (c = lane % 16, h = lane / 16):
 //   * S^T = K Q^T: first operand 16 keys (lane c: key c, 8 values of it),
@@ -125,39 +126,30 @@ struct DecodeArgs {
   const int32_t *pages, *lens;
   const void* Q;
   void* O;
-  float* part;  // per (piece, column): 16 x D sums, then 16 x (maximum, sum)
+  float* part;  // two pieces per workgroup: 16 x D sums, then 16 x (maximum, sum)
   int64_t ld, ldq, ldo;
   int num_pages, page_size, heads, width, batch;
   int group;   // query heads per key head
   int qtiles;  // tiles of 16 of them
-  int target;  // pieces aimed at
+  int workgroups;
   Divider groups;  // by the groups of 16 tokens of a page
   float scale_log2;
 };
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
-// The split of the batch's keys into pieces, found by each wave for itself:
-// lane l counts for sequences l * per .. + per - 1.
-struct Split {
+// The batch's units, counted by each wave for itself: lane l for sequences
+// l * per .. + per - 1.
+struct Units {
   int per, i0, i1;  // this lane's sequences
-  int unit;         // units per piece
-  int own, before;  // pieces of this lane's sequences, and of those before them
+  int own, before;  // units of this lane's sequences, and of those before them
+  int total;
 };
-__device__ __forceinline__ Split split_batch(const int32_t* lens, int batch, int cap, int target, int lane) {
-  Split s;
+__device__ __forceinline__ Units count_units(const int32_t* lens, int batch, int cap, int lane) {
+  Units s;
   s.per = (batch + 63) / 64;
   s.i0 = min(lane * s.per, batch);
   s.i1 = min(s.i0 + s.per, batch);
-  int units = 0;
-  for (int i = s.i0; i < s.i1; ++i) units += units_of(seq_len(lens[i], cap));
-  s.unit = piece_units(wave_sum(units), target);
   s.own = 0;
-  for (int i = s.i0; i < s.i1; ++i) s.own += pieces_of(units_of(seq_len(lens[i], cap)), s.unit);
+  for (int i = s.i0; i < s.i1; ++i) s.own += units_of(seq_len(lens[i], cap));
   int incl = s.own;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -165,12 +157,15 @@ __device__ __forceinline__ Split split_batch(const int32_t* lens, int batch, int
     if (lane >= d) incl += up;
   }
   s.before = incl - s.own;
+  s.total = __builtin_amdgcn_readlane(incl, 63);
   return s;
 }
 
+// Piece `which` of workgroup w: 0 of a sequence that began in an earlier
+// workgroup's share, 1 of one that begins in this one's and ends later.
 template <int D>
-__device__ __forceinline__ float* part_of(const DecodeArgs& a, int piece, int column, int columns) {
-  return a.part + ((int64_t)piece * columns + column) * (16 * (D + 2));
+__device__ __forceinline__ float* part_of(const DecodeArgs& a, int w, int which) {
+  return a.part + ((int64_t)w * 2 + which) * (16 * (D + 2));
 }
 
 // 8-bit codes 2 HI and 2 HI + 1 of src as two 16-bit values, times the
@@ -210,34 +205,55 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   const int c = lane & 15, h = lane >> 4;
   const int cap = a.width * a.page_size;
 
-  // the piece: the lane whose sequences hold piece blockIdx.x walks to it
-  const Split sp = split_batch(a.lens, a.batch, cap, a.target, lane);
-  const int piece = blockIdx.x;
-  const uint64_t owner = __builtin_amdgcn_ballot_w64(piece >= sp.before && piece < sp.before + sp.own);
-  if (owner == 0) return;
-  int seq = sp.i0, at = sp.before, count = 0;
-  for (int i = sp.i0; i < sp.i1; ++i) {
-    const int n = pieces_of(units_of(seq_len(a.lens[i], cap)), sp.unit);
-    if (piece < at + n) {
-      seq = i;
-      count = n;
-      break;
-    }
-    at += n;
+  const int columns = a.heads * a.qtiles;
+  const int w = blockIdx.x;
+  const Units un = count_units(a.lens, a.batch, cap, lane);
+  // an empty sequence has no units: its zeros are written here
+  for (int i = w; i < a.batch * columns; i += a.workgroups) {
+    const int seq = i / columns, col = i % columns;
+    if (seq_len(a.lens[seq], cap) != 0) continue;
+    const int qh = (col % a.qtiles) * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * VEC;
+    if (qh >= a.group) continue;
+    T* op = (T*)a.O + seq * a.ldo + (int64_t)((col / a.qtiles) * a.group + qh) * D + d0;
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = 0u;
   }
-  const int src = __builtin_ctzll(owner);
-  seq = __builtin_amdgcn_readlane(seq, src);
-  count = __builtin_amdgcn_readlane(count, src);
-  const int index = piece - __builtin_amdgcn_readlane(at, src);
-  const int unit = __builtin_amdgcn_readfirstlane(sp.unit);
-  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lens[seq], cap));
-  // (units up to the cap fit an int; the last piece's end need not)
-  const int kbeg = index * unit * kUnit;
-  const int kend = (int)min((int64_t)len, (int64_t)(index + 1) * unit * kUnit);
+  const int64_t F = (int64_t)un.total * columns;
+  const int shares = sharers(F, a.workgroups);
+  if (w >= shares) return;
+  int64_t f = share_begin(F, w, shares);
+  const int64_t fend = share_begin(F, w + 1, shares);
+  int column = (int)(f / un.total), u = (int)(f % un.total);  // unit u of this column is next
+  // its sequence: the lane that counted it walks there
+  int seq, begin;  // the sequence, and the number of its first unit in a column
+  {
+    const uint64_t owner = __builtin_amdgcn_ballot_w64(u >= un.before && u < un.before + un.own);
+    int i = un.i0, at = un.before;
+    while (i < un.i1) {
+      const int n = units_of(seq_len(a.lens[i], cap));
+      if (u < at + n) break;
+      at += n;
+      ++i;
+    }
+    const int src = __builtin_ctzll(owner);
+    seq = __builtin_amdgcn_readlane(i, src);
+    begin = __builtin_amdgcn_readlane(at, src);
+  }
+  for (; f < fend; ) {
+  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lens[seq], cap)), units = units_of(len);
+  if (units == 0) {
+    if (++seq == a.batch) {
+      seq = 0;
+      ++column;
+      begin = u = 0;
+    }
+    continue;
+  }
+  const int take = (int)min(fend - f, (int64_t)(begin + units - u));
+  const int kbeg = (u - begin) * kUnit, kend = min(len, kbeg + take * kUnit);
 
   // the query heads of this column
-  const int columns = a.heads * a.qtiles;
-  const int head = blockIdx.y / a.qtiles, first = (blockIdx.y % a.qtiles) * 16;
+  const int head = column / a.qtiles, first = (column % a.qtiles) * 16;
   const bool query = first + c < a.group;
   const T* q = (const T*)a.Q + seq * a.ldq + (int64_t)(head * a.group + first + c) * D;
   u32x4 qf[KS];
@@ -414,76 +430,106 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
     for (int e = 0; e < 4; ++e) so[wave][c][VEC * (4 * h + e) + j] = acc[j][e];
   __syncthreads();
   const int qh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * VEC;
-  if (first + qh >= a.group) return;
-  const float mj = fmaxf(fmaxf(sm[0][qh], sm[1][qh]), fmaxf(sm[2][qh], sm[3][qh]));
-  const float ref = mj == kNegInf ? 0.0f : mj;
-  float o[VEC] = {}, lj = 0.0f;
+  if (first + qh < a.group) {
+    const float mj = fmaxf(fmaxf(sm[0][qh], sm[1][qh]), fmaxf(sm[2][qh], sm[3][qh]));
+    const float ref = mj == kNegInf ? 0.0f : mj;
+    float o[VEC] = {}, lj = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = __builtin_amdgcn_exp2f(sm[w][qh] - ref);
-    lj += f * sl[w][qh];
+    for (int i = 0; i < 4; ++i) {
+      const float x = __builtin_amdgcn_exp2f(sm[i][qh] - ref);
+      lj += x * sl[i][qh];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] += f * so[w][qh][d0 + j];
-  }
-  if (count == 1) {
-    const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
-    T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
+      for (int j = 0; j < VEC; ++j) o[j] += x * so[i][qh][d0 + j];
+    }
+    if (take == units) {
+      const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
+      T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
 #pragma unroll
-    for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
-  } else {
-    float* pp = part_of<D>(a, piece, blockIdx.y, columns);
+      for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
+    } else {
+      float* pp = part_of<D>(a, w, u == begin);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) pp[qh * D + d0 + j] = o[j];
-    if (d0 == 0) {
-      pp[16 * D + 2 * qh] = mj;
-      pp[16 * D + 2 * qh + 1] = lj;
+      for (int j = 0; j < VEC; ++j) pp[qh * D + d0 + j] = o[j];
+      if (d0 == 0) {
+        pp[16 * D + 2 * qh] = mj;
+        pp[16 * D + 2 * qh + 1] = lj;
+      }
     }
   }
+  f += take;
+  u += take;
+  if (u == begin + units) {
+    begin = u;
+    if (++seq == a.batch) {
+      seq = 0;
+      ++column;
+      begin = u = 0;
+    }
+  }
+  if (f < fend) __syncthreads();  // the waves' sums have been read
+  }
 }
 
-// Joins the pieces of one sequence and column, in their order.
+// Joins the pieces of one sequence and query head, in their order: eight
+// groups of threads take every eighth piece, then add up in LDS.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
-  constexpr int VEC = D / 16;
+  constexpr int LPP = D / 4, GROUPS = 256 / LPP;  // lanes of a piece, pieces at once
+  __shared__ float smax[4], sl[GROUPS];
+  __shared__ f32x4 so[GROUPS][LPP];
   const int lane = threadIdx.x & 63;
-  const int cap = a.width * a.page_size, seq = blockIdx.x;
-  const Split sp = split_batch(a.lens, a.batch, cap, a.target, lane);
-  const int count = pieces_of(units_of(seq_len(a.lens[seq], cap)), sp.unit);
-  if (count == 1) return;
-  int at = sp.before;
-  for (int i = sp.i0; i < sp.i1 && i < seq; ++i) at += pieces_of(units_of(seq_len(a.lens[i], cap)), sp.unit);
-  const int piece = __builtin_amdgcn_readlane(at, seq / sp.per);
+  const int cap = a.width * a.page_size, seq = blockIdx.x, qhead = blockIdx.y;
+  const int units = units_of(seq_len(a.lens[seq], cap));
+  if (units == 0) return;
+  const Units un = count_units(a.lens, a.batch, cap, lane);
+  int at = un.before;
+  for (int i = un.i0; i < un.i1 && i < seq; ++i) at += units_of(seq_len(a.lens[i], cap));
+  const int begin = __builtin_amdgcn_readlane(at, seq / un.per);
+  const int head = qhead / a.group, qg = qhead % a.group, row = qg % 16;
   const int columns = a.heads * a.qtiles;
-  const int head = blockIdx.y / a.qtiles, first = (blockIdx.y % a.qtiles) * 16;
-  const int qh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * VEC;
-  if (first + qh >= a.group) return;
+  const int64_t F = (int64_t)un.total * columns, f0 = (int64_t)un.total * (head * a.qtiles + qg / 16) + begin;
+  const int shares = sharers(F, a.workgroups);
+  const int w0 = share_of(F, f0, shares), count = share_of(F, f0 + units - 1, shares) - w0 + 1;
+  if (count == 1) return;
+  auto piece = [&](int p) { return part_of<D>(a, w0 + p, p == 0); };
   float m = kNegInf;
-  for (int p = 0; p < count; ++p) m = fmaxf(m, part_of<D>(a, piece + p, blockIdx.y, columns)[16 * D + 2 * qh]);
+  for (int p = threadIdx.x; p < count; p += 256) m = fmaxf(m, piece(p)[16 * D + 2 * row]);
+  m = wave::all<wave::Max>(m);
+  if (lane == 0) smax[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
   const float ref = m == kNegInf ? 0.0f : m;
-  float o[VEC] = {}, l = 0.0f;
-  for (int p = 0; p < count; ++p) {
-    const float* pp = part_of<D>(a, piece + p, blockIdx.y, columns);
-    const float f = __builtin_amdgcn_exp2f(pp[16 * D + 2 * qh] - ref);
-    l += f * pp[16 * D + 2 * qh + 1];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] += f * pp[qh * D + d0 + j];
+  const int g = threadIdx.x / LPP, t = threadIdx.x % LPP;
+  f32x4 o = {};
+  float l = 0.0f;
+#pragma unroll 4
+  for (int p = g; p < count; p += GROUPS) {
+    const float* pp = piece(p);
+    const float x = __builtin_amdgcn_exp2f(pp[16 * D + 2 * row] - ref);
+    l += x * pp[16 * D + 2 * row + 1];
+    o += x * *(const f32x4*)(pp + row * D + 4 * t);
+  }
+  so[g][t] = o;
+  if (t == 0) sl[g] = l;
+  __syncthreads();
+  if (g != 0) return;
+  for (int i = 1; i < GROUPS; ++i) {
+    o += so[i][t];
+    l += sl[i];
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
-#pragma unroll
-  for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
+  T* op = (T*)a.O + seq * a.ldo + (int64_t)qhead * D + 4 * t;
+  *(u32x2*)op = u32x2{pack2_out<T>(o[0] * inv, o[1] * inv), pack2_out<T>(o[2] * inv, o[3] * inv)};
 }
 
-constexpr int kWorkgroups = 1024;  // aimed at: four for each of the 256 CUs
+constexpr int kWorkgroups = 512;  // two for each of the 256 CUs
 
 template <typename T, bool FP8, int D>
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream) {
-  const int columns = a.heads * a.qtiles;
-  const int64_t pieces = piece_bound(a.batch, (int64_t)a.width * a.page_size, a.target);
-  hipLaunchKernelGGL((decode_kernel<T, FP8, D>), dim3((unsigned)pieces, columns), dim3(256), 0, stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || pieces == a.batch) return e;
-  hipLaunchKernelGGL((join_kernel<T, D>), dim3(a.batch, columns), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((decode_kernel<T, FP8, D>), dim3(a.workgroups), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((join_kernel<T, D>), dim3(a.batch, a.heads * a.group), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -541,20 +587,19 @@ bool formats_fit(const gemm_epi_paged_cache* c, gemm_epi_dtype dtype) {
 }
 
 struct Shape {
-  int group, qtiles, target;
-  int64_t pieces;
+  int group, qtiles, workgroups;
 };
 Shape shape_of(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
   Shape s;
   s.group = (int)(q_heads / c->heads);
   s.qtiles = (s.group + 15) / 16;
-  s.target = piece_target((int)c->heads * s.qtiles, kWorkgroups);
-  s.pieces = piece_bound(batch, width * c->page_size, s.target);
+  // no more workgroups than units
+  const int64_t units = batch * ((width * c->page_size + kUnit - 1) / kUnit) * c->heads * s.qtiles;
+  s.workgroups = (int)(units < kWorkgroups ? units : kWorkgroups);
   return s;
 }
 size_t workspace_bytes(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
-  const Shape s = shape_of(c, batch, width, q_heads);
-  return (size_t)s.pieces * (size_t)(c->heads * s.qtiles) * (size_t)(16 * (c->head_dim + 2)) * 4;
+  return (size_t)shape_of(c, batch, width, q_heads).workgroups * 2 * (size_t)(16 * (c->head_dim + 2)) * 4;
 }
 
 template <typename T, bool FP8>
@@ -648,7 +693,7 @@ gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, con
                      (int)table->batch,
                      sh.group,
                      sh.qtiles,
-                     sh.target,
+                     sh.workgroups,
                      make_divider((int)cache->page_size / 16),
                      (float)(1.4426950408889634 / __builtin_sqrt((double)d))};
   const hipStream_t st = (hipStream_t)stream;

@@ -200,10 +200,9 @@ int c_divide(int n, int d) { return divide(n, make_divider(d)); }
 int64_t c_row_of(int p, int hs, int h, int ps, int s) { return row_of(p, hs, h, ps, s); }
 int c_new_position(int len, int end, int row, int cap) { return new_position(len, end, row, cap); }
 int c_units_of(int len) { return units_of(len); }
-int c_piece_units(int total, int target) { return piece_units(total, target); }
-int c_pieces_of(int units, int per) { return pieces_of(units, per); }
-int c_piece_target(int columns, int wgs) { return piece_target(columns, wgs); }
-int64_t c_piece_bound(int64_t batch, int64_t cap, int target) { return piece_bound(batch, cap, target); }
+int c_sharers(int64_t F, int n) { return sharers(F, n); }
+int64_t c_share_begin(int64_t F, int w, int n) { return share_begin(F, w, n); }
+int c_share_of(int64_t F, int64_t f, int n) { return share_of(F, f, n); }
 }
 '''
 
@@ -219,8 +218,10 @@ def paged(tmp_path_factory):
     assert r.returncode == 0, r.stderr
     lib = ctypes.CDLL(str(so))
     lib.c_row_of.restype = ctypes.c_int64
-    lib.c_piece_bound.restype = ctypes.c_int64
-    lib.c_piece_bound.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+    lib.c_share_begin.restype = ctypes.c_int64
+    lib.c_share_begin.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    lib.c_sharers.argtypes = [ctypes.c_int64, ctypes.c_int]
+    lib.c_share_of.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     return lib
 
 
@@ -259,38 +260,22 @@ def test_new_positions(paged):
             assert paged.c_new_position(length, end, row, cap) == (p if 0 <= p < cap else -1)
 
 
+def test_units(paged):
+    for n in (0, 1, 127, 128, 129, 4096, INT_MAX - 256, INT_MAX):
+        assert paged.c_units_of(n) == -(-n // 128)
+
+
 @pytest.mark.parametrize("seed", range(40))
-def test_pieces_cover_every_key_once_within_the_bound(paged, seed):
+def test_shares_cover_every_unit_once(paged, seed):
     rng = np.random.default_rng(seed)
-    batch = int(rng.integers(1, 200))
-    cap = int(rng.choice([16, 48, 128, 1000 * 16, 131072]))
-    lens = rng.integers(-5, int(cap * 1.2), size=batch)
-    if seed % 3 == 0:
-        lens[rng.random(batch) < 0.5] = 0
-    if seed % 5 == 0:
-        lens[:] = cap
-    columns = int(rng.choice([1, 2, 8, 64, 1024, 2000]))
-    target = paged.c_piece_target(columns, 1024)
-    assert 1 <= target <= 1024
-    lens = [paged.c_seq_len(int(n), cap) for n in lens]
-    units = [paged.c_units_of(n) for n in lens]
-    assert units == [-(-n // 128) for n in lens]
-    per = paged.c_piece_units(sum(units), target)
-    counts = [paged.c_pieces_of(u, per) for u in units]
-    assert sum(counts) <= paged.c_piece_bound(batch, cap, target)
-    assert min(counts) >= 1
-    for n, u, k in zip(lens, units, counts):
-        # piece i holds keys [i * per * 128, min(n, (i + 1) * per * 128))
-        ends = [min(n, (i + 1) * per * 128) for i in range(k)]
-        begins = [i * per * 128 for i in range(k)]
-        assert ends[-1] == n and (n == 0 or all(b < e for b, e in zip(begins, ends)))
-        assert all(e == b for e, b in zip(ends[:-1], begins[1:]))
-
-
-def test_extreme_splits(paged):
-    top = ((1 << 31) - 256 + 127) // 128
-    per = paged.c_piece_units(top, 1)
-    assert per == top and paged.c_pieces_of(top, per) == 1
-    assert paged.c_piece_units(INT_MAX, 1024) * 1024 >= INT_MAX
-    assert paged.c_piece_bound(65535, 16, 1024) == 65535
-    assert paged.c_units_of(INT_MAX) == 1 << 24
+    F = int(rng.choice([1, 2, 7, 511, 512, 513, 100003, 1 << 31, (1 << 31) * 2048 - 5]))
+    given = int(rng.choice([1, 2, 8, 63, 512, 1024]))
+    W = paged.c_sharers(F, given)
+    assert W == min(F, given)
+    begins = [paged.c_share_begin(F, w, W) for w in range(W + 1)]
+    assert begins[0] == 0 and begins[-1] == F
+    sizes = np.diff(begins)
+    assert sizes.min() >= 1 and sizes.max() - sizes.min() <= 1  # even
+    for f in {0, F - 1, *[int(x) for x in rng.integers(0, F, 50)], *[b for b in begins if b < F], *[b - 1 for b in begins if b > 0]}:
+        w = paged.c_share_of(F, f, W)
+        assert begins[w] <= f < begins[w + 1], (F, W, f)
