@@ -178,14 +178,15 @@ __device__ __forceinline__ uint32_t widen2(uint32_t src, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, scale, HI));
 }
 
-// A tile of 32 keys as loaded: for each group of 16 its key row of this lane
-// and (u = 4 g + 0..3) the V rows of this lane, and how many of the group's
-// keys exist.
+// A tile of 32 keys as loaded: of each group of 16, whose K rows are
+// contiguous, this lane's 16 bytes of every KiB; (u = 4 g + 0..3) this lane's
+// part of V's rows; and how many of the group's keys exist.
 template <bool FP8, int D>
 struct Tile {
   static constexpr int VEC = D / 16;        // values of a row per lane in V's operand
   static constexpr int EB = FP8 ? 1 : 2;    // bytes of a cache element
-  static constexpr int KL = D * EB / 64;    // 16-byte loads of a lane for its key
+  static constexpr int RB = D * EB;         // bytes of a cache row
+  static constexpr int KL = RB / 64;        // KiB of a group's K
   static constexpr int VW = VEC * EB / 4;   // 32-bit words of a lane for one key's V
   typedef uint32_t vwords __attribute__((ext_vector_type(VW == 1 ? 2 : VW)));  // (one word: in .x)
   u32x4 k[2][KL];
@@ -198,9 +199,14 @@ struct Tile {
 template <typename T, bool FP8, int D>
 __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   using Tl = Tile<FP8, D>;
-  constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW;
+  constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW, RB = Tl::RB;
   constexpr int KS = D / 32;  // 32-deep steps of a score
   __shared__ float sm[4][16], sl[4][16], so[4][16][D + 4];
+  // K's rows change lanes through LDS, each wave's in its own part: loaded in
+  // whole KiB, read as MFMA operands (lane (c, h): 16 bytes of row c).  Chunk
+  // x of row r stands at x ^ (r RB / 256), so that the 16 rows of a read fall
+  // on different banks.
+  __shared__ __attribute__((aligned(1024))) char sk[4][32 * RB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
   const int cap = a.width * a.page_size;
@@ -278,7 +284,13 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
     for (int g = 0; g < 2; ++g) p.g[g] = table[divide((k0 + 16 * g < kend ? k0 + 16 * g : k0) >> 4, a.groups)];
     return p;
   };
-  const uint32_t koff = (uint32_t)(c * D * EB + 16 * h), voff = (uint32_t)(4 * h * D * EB + c * VEC * EB);
+  constexpr int CPR = RB / 16;  // chunks of a row
+  auto kwrite = [&](int i) __attribute__((always_inline)) {
+    const int r = lane / CPR + i * (1024 / RB);
+    return r * RB + (((lane % CPR) ^ (r * RB / 256 % CPR)) << 4);
+  };
+  auto kread = [&](int i) __attribute__((always_inline)) { return c * RB + (((4 * i + h) ^ (c * RB / 256 % CPR)) << 4); };
+  const uint32_t koff = (uint32_t)(16 * lane), voff = (uint32_t)(4 * h * D * EB + c * VEC * EB);
   auto load = [&](Tl& t, int k0, Pages p) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
@@ -290,12 +302,12 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       const char* kp = a.k + row * (D * EB);
       const char* vp = a.v + row * (D * EB);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) t.k[g][i] = *(const u32x4*)(kp + koff + 64 * i);
+      for (int i = 0; i < KL; ++i) t.k[g][i] = __builtin_nontemporal_load((const u32x4*)(kp + koff + 1024 * i));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const char* r = vp + voff + u * D * EB;
         if constexpr (VW == 1) t.v[4 * g + u].x = *(const uint32_t*)r;
-        else t.v[4 * g + u] = *(const typename Tl::vwords*)r;
+        else t.v[4 * g + u] = __builtin_nontemporal_load((const typename Tl::vwords*)r);
       }
       if constexpr (FP8) {
         t.ks[g] = a.ks[row + c];
@@ -306,14 +318,23 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   auto multiply = [&](const Tl& t) __attribute__((always_inline)) {
     const bool whole = t.valid[0] == 16 && t.valid[1] == 16;
     // scores
+    char* const kl = sk[wave];
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int i = 0; i < KL; ++i) *(u32x4*)(kl + g * 16 * RB + kwrite(i)) = t.k[g][i];
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses are done in order)
     f32x4 s[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       s[g] = f32x4{};
+      u32x4 kf[KL];
+#pragma unroll
+      for (int i = 0; i < KL; ++i) kf[i] = *(const u32x4*)(kl + g * 16 * RB + kread(i));
       if constexpr (FP8) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
-          const u32x4 x = t.k[g][i];
+          const u32x4 x = kf[i];
           const float f = t.ks[g];
           const u32x4 lo = {widen2<T, false>(x[0], f), widen2<T, true>(x[0], f), widen2<T, false>(x[1], f),
                             widen2<T, true>(x[1], f)};
@@ -324,7 +345,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(t.k[g][i], qf[i], s[g]);
+        for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(kf[i], qf[i], s[g]);
       }
       s[g] *= a.scale_log2;
     }
