@@ -299,6 +299,9 @@ def gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads) -> in
     return int(load_library().gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads))
 
 
+ATTENTION_DECODE_COUNTER_BYTES = 2048  # GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES
+
+
 # What the tensor calls below check is cheap to compare and slow to explain:
 # they compare inline and come here only to say what was wrong.
 
@@ -366,15 +369,15 @@ def _device_and_stream(torch, stream):
     return index, stream.cuda_stream
 
 
-def _workspace(torch, workspace, need, index, stream):
-    """(pointer, bytes) of the caller's workspace, or of one of `need()` bytes
-    from torch's allocator on the stream of the call."""
+def _workspace(torch, workspace, need, index, stream, zeros=0):
+    """(pointer, bytes) of the caller's workspace, or of one of `need()` bytes,
+    the first `zeros` of them zero, from torch's allocator on the stream of
+    the call."""
     if workspace is None:
-        if stream is None:
+        with torch.cuda.stream(stream):  # (None: the current one)
             workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
+            if zeros:
+                workspace[:zeros].zero_()
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {index}")
     return workspace.data_ptr(), workspace.nbytes
@@ -528,7 +531,9 @@ class PagedCache:
         (0 where there are none).  q and o [batch, q_heads, head_dim] (rows
         may be strided), float16 or bfloat16, the cache's format unless that
         is float8_e4m3fn.  ``workspace``: an optional CUDA tensor of
-        ``workspace_size`` bytes, else one is allocated."""
+        ``workspace_size`` bytes, its first ATTENTION_DECODE_COUNTER_BYTES
+        zero before its first use (every completed run leaves them zero), else
+        one is allocated."""
         import torch
 
         index, s = _device_and_stream(torch, stream)
@@ -542,7 +547,8 @@ class PagedCache:
         ldq, ldo = _rows3("q", q, dt, shape, index), _rows3("o", o, dt, shape, index)
         if batch == 0:
             return
-        ws, nbytes = _workspace(torch, workspace, lambda: self.workspace_size(heads, pages), index, stream)
+        ws, nbytes = _workspace(torch, workspace, lambda: self.workspace_size(heads, pages), index, stream,
+                                ATTENTION_DECODE_COUNTER_BYTES)
         st = (_lib or load_library()).gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(),
                                                                 ldo, heads, fmt, ws, nbytes, s)
         if st != OK:

@@ -55,15 +55,41 @@ GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 
 // The keys of a batch are split evenly over its workgroups: with U the units
 // of all sequences and `columns` the (key head, query tile) pairs, unit u of
-// column c has number f = c U + u, and workgroup w takes numbers
-// share_begin(F, w) to share_begin(F, w + 1) - 1 of F = columns * U.  A
-// sequence's units in one column are then cut into pieces where shares end.
-// No workgroup has an empty share: of more workgroups than units the first F
+// column c has number f = c U + u, of F = columns * U < 2^31 numbers, and each
+// workgroup takes a share of consecutive ones: F / n each, the first F % n
+// one more.  A sequence's units in one column are then cut into pieces where
+// shares end.  No share is empty: of more workgroups than units the first F
 // take one each.
-GE_HD int sharers(int64_t F, int workgroups) { return F < workgroups ? (int)F : workgroups; }
-GE_HD int64_t share_begin(int64_t F, int w, int workgroups) { return F * w / workgroups; }
-// The workgroup that has number f.
-GE_HD int share_of(int64_t F, int64_t f, int workgroups) { return (int)(((f + 1) * workgroups - 1) / F); }
+struct Shares {
+  int n, base, more;  // shares, numbers in each, and how many have one more
+};
+GE_HD Shares make_shares(int F, int workgroups) {
+  const int n = F < workgroups ? F : workgroups;
+  return n == 0 ? Shares{0, 0, 0} : Shares{n, (int)((uint32_t)F / (uint32_t)n), (int)((uint32_t)F % (uint32_t)n)};
+}
+GE_HD int share_begin(Shares s, int w) { return w * s.base + (w < s.more ? w : s.more); }
+// The share that has number f < F.
+GE_HD int share_of(Shares s, int f) {
+  const uint32_t base = (uint32_t)s.base, big = (uint32_t)s.more * (base + 1);
+  return (uint32_t)f < big ? (int)((uint32_t)f / (base + 1)) : s.more + (int)(((uint32_t)f - big) / base);
+}
+
+// The pieces of a cut sequence are joined by the last of its workgroups when
+// that takes at most kRounds rounds of loads (a round: kBatch pieces for each
+// group of threads, a group being rows * head_dim / 4 of the 256), else by
+// the join kernel.
+constexpr int kBatch = 16, kRounds = 4;
+GE_HD bool joined_here(int pieces, int rows, int head_dim) {
+  const int most = 1024 / head_dim;  // rows at a time
+  const int passes = (rows + most - 1) / most, groups = rows < most ? most / rows : 1;
+  return passes * ((pieces + kBatch * groups - 1) / (kBatch * groups)) <= kRounds;
+}
+// The most pieces a sequence of up to `cap` tokens can be cut into: one per
+// unit, and one per share of a column and the two it ends in.
+GE_HD int64_t pieces_bound(int64_t cap, int columns, int workgroups) {
+  const int64_t units = (cap + kUnit - 1) / kUnit, shares = workgroups / columns + 2;
+  return units < shares ? units : shares;
+}
 
 }  // namespace paged
 }  // namespace ge

@@ -120,12 +120,22 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------------------
 // decode attention
 // ---------------------------------------------------------------------------
+// Workgroups of the decode attention: those the memory system wants in flight
+// at once.  Rows of 256 bytes: one for each of the 256 CUs (its waves then
+// have 64 to 128 KiB in flight; 32 x 8192 bf16, D = 128: 96 us, two for each
+// 102); shorter rows: two (8 x 65536 E4M3, D = 128: 115 against 151 us; 128 x
+// 2047 f16, D = 64: 108 against 116).
+constexpr int kWorkgroups = 512;
+inline int workgroups_for(int row_bytes) { return row_bytes == 256 ? 256 : kWorkgroups; }
+static_assert(kWorkgroups * 4 == GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES, "a counter each");
+
 struct DecodeArgs {
   const char *k, *v;
   const float *ks, *vs;
   const int32_t *pages, *lens;
   const void* Q;
   void* O;
+  unsigned* arrivals;  // kWorkgroups counters, zero between runs
   float* part;  // two pieces per workgroup: 16 x D sums, then 16 x (maximum, sum)
   int64_t ld, ldq, ldo;
   int num_pages, page_size, heads, width, batch;
@@ -140,25 +150,35 @@ struct DecodeArgs {
 // l * per .. + per - 1.
 struct Units {
   int per, i0, i1;  // this lane's sequences
+  int len;          // tokens of the first of them
   int own, before;  // units of this lane's sequences, and of those before them
   int total;
+  bool empty;  // some sequence of the batch has no tokens
 };
 __device__ __forceinline__ Units count_units(const int32_t* lens, int batch, int cap, int lane) {
   Units s;
   s.per = (batch + 63) / 64;
   s.i0 = min(lane * s.per, batch);
   s.i1 = min(s.i0 + s.per, batch);
-  s.own = 0;
-  for (int i = s.i0; i < s.i1; ++i) s.own += units_of(seq_len(lens[i], cap));
-  int incl = s.own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(incl, d);
-    if (lane >= d) incl += up;
+  s.own = s.len = 0;
+  bool none = false;
+  for (int i = s.i0; i < s.i1; ++i) {
+    const int n = seq_len(lens[i], cap);
+    if (i == s.i0) s.len = n;
+    none |= n == 0;
+    s.own += units_of(n);
   }
+  const int incl = wave::scan(s.own);
   s.before = incl - s.own;
   s.total = __builtin_amdgcn_readlane(incl, 63);
+  s.empty = __builtin_amdgcn_ballot_w64(none) != 0;
   return s;
+}
+// Tokens of sequence seq (the same in every lane): from the lanes where each
+// has one.
+__device__ __forceinline__ int len_of(const Units& un, const int32_t* lens, int seq, int cap) {
+  return un.per == 1 ? __builtin_amdgcn_readlane(un.len, seq)
+                     : __builtin_amdgcn_readfirstlane(seq_len(lens[seq], cap));
 }
 
 // Piece `which` of workgroup w: 0 of a sequence that began in an earlier
@@ -166,6 +186,66 @@ __device__ __forceinline__ Units count_units(const int32_t* lens, int batch, int
 template <int D>
 __device__ __forceinline__ float* part_of(const DecodeArgs& a, int w, int which) {
   return a.part + ((int64_t)w * 2 + which) * (16 * (D + 2));
+}
+
+// Joins `rows` rows from `row0` on of a cut sequence's pieces, in their
+// order, into o[row - row0][D]: a row is D / 4 threads', and what threads
+// remain make further groups that take every n-th piece each and add up in
+// LDS (256 x 6 floats), so that many loads are in flight.  rows * D / 4 <= 256.
+template <typename T, int D>
+__device__ __forceinline__ void join_rows(const DecodeArgs& a, int w0, int pieces, int row0, int rows, T* o, float* lds) {
+  constexpr int LPR = D / 4;
+  const int slots = rows * LPR, groups = 256 / slots;
+  const int g = threadIdx.x / slots, slot = threadIdx.x % slots, row = row0 + slot / LPR, t = slot % LPR;
+  float m = kNegInf, l = 0.0f;
+  f32x4 s = {};
+  auto add = [&](float mp, float lp, f32x4 sp) __attribute__((always_inline)) {
+    const float mn = fmaxf(m, mp), ref = mn == kNegInf ? 0.0f : mn;
+    const float x = __builtin_amdgcn_exp2f(m - ref), y = __builtin_amdgcn_exp2f(mp - ref);
+    m = mn;
+    l = l * x + lp * y;
+    s = s * x + sp * y;
+  };
+  if (g < groups) {
+    // a round's loads at a time (past the last piece: a maximum of -inf)
+    for (int p0 = g; p0 < pieces; p0 += kBatch * groups) {
+      float mp[kBatch], lp[kBatch];
+      f32x4 sp[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int p = min(p0 + i * groups, pieces - 1);
+        const float* pp = part_of<D>(a, w0 + p, p == 0);
+        mp[i] = p0 + i * groups < pieces ? pp[16 * D + 2 * row] : kNegInf;
+        lp[i] = pp[16 * D + 2 * row + 1];
+        sp[i] = *(const f32x4*)(pp + row * D + 4 * t);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add(mp[i], lp[i], sp[i]);
+    }
+    f32x4* ls = (f32x4*)lds + threadIdx.x;
+    *ls = s;
+    lds[1024 + 2 * threadIdx.x] = m;
+    lds[1024 + 2 * threadIdx.x + 1] = l;
+  }
+  __syncthreads();
+  if (g == 0) {
+    for (int i = 1; i < groups; ++i) {
+      const int th = i * slots + slot;
+      add(lds[1024 + 2 * th], lds[1024 + 2 * th + 1], ((const f32x4*)lds)[th]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *(u32x2*)(o + (row - row0) * D + 4 * t) = u32x2{pack2_out<T>(s[0] * inv, s[1] * inv), pack2_out<T>(s[2] * inv, s[3] * inv)};
+  }
+}
+
+// All rows of a cut sequence's pieces.
+template <typename T, int D>
+__device__ __forceinline__ void join_pieces(const DecodeArgs& a, int w0, int pieces, int rows, T* o, float* lds) {
+  constexpr int most = 1024 / D;  // rows at a time
+  for (int r = 0; r < rows; r += most) {
+    join_rows<T, D>(a, w0, pieces, r, min(most, rows - r), o + r * D, lds);
+    __syncthreads();  // the sums in LDS have been read
+  }
 }
 
 // 8-bit codes 2 HI and 2 HI + 1 of src as two 16-bit values, times the
@@ -201,7 +281,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   using Tl = Tile<FP8, D>;
   constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW, RB = Tl::RB;
   constexpr int KS = D / 32;  // 32-deep steps of a score
-  __shared__ float sm[4][16], sl[4][16], so[4][16][D + 4];
+  __shared__ float sm[4][16], sl[4][16];
+  __shared__ __attribute__((aligned(16))) float so[4][16][D + 4];
+  __shared__ int last_arrived;
   // K's rows change lanes through LDS, each wave's in its own part: loaded in
   // whole KiB, read as MFMA operands (lane (c, h): 16 bytes of row c).  Chunk
   // x of row r stands at x ^ (r RB / 256), so that the 16 rows of a read fall
@@ -215,21 +297,21 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   const int w = blockIdx.x;
   const Units un = count_units(a.lens, a.batch, cap, lane);
   // an empty sequence has no units: its zeros are written here
-  for (int i = w; i < a.batch * columns; i += a.workgroups) {
-    const int seq = i / columns, col = i % columns;
-    if (seq_len(a.lens[seq], cap) != 0) continue;
-    const int qh = (col % a.qtiles) * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * VEC;
-    if (qh >= a.group) continue;
-    T* op = (T*)a.O + seq * a.ldo + (int64_t)((col / a.qtiles) * a.group + qh) * D + d0;
+  if (un.empty)
+    for (int i = w; i < a.batch * columns; i += gridDim.x) {
+      const int seq = i / columns, col = i % columns;
+      if (seq_len(a.lens[seq], cap) != 0) continue;
+      const int qh = (col % a.qtiles) * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * VEC;
+      if (qh >= a.group) continue;
+      T* op = (T*)a.O + seq * a.ldo + (int64_t)((col / a.qtiles) * a.group + qh) * D + d0;
 #pragma unroll
-    for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = 0u;
-  }
-  const int64_t F = (int64_t)un.total * columns;
-  const int shares = sharers(F, a.workgroups);
-  if (w >= shares) return;
-  int64_t f = share_begin(F, w, shares);
-  const int64_t fend = share_begin(F, w + 1, shares);
-  int column = (int)(f / un.total), u = (int)(f % un.total);  // unit u of this column is next
+      for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = 0u;
+    }
+  const Shares sh = make_shares(un.total * columns, gridDim.x);
+  if (w >= sh.n) return;
+  int f = share_begin(sh, w);
+  const int fend = share_begin(sh, w + 1);
+  int column = (int)((uint32_t)f / (uint32_t)un.total), u = f - column * un.total;  // unit u of this column is next
   // its sequence: the lane that counted it walks there
   int seq, begin;  // the sequence, and the number of its first unit in a column
   {
@@ -245,8 +327,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
     seq = __builtin_amdgcn_readlane(i, src);
     begin = __builtin_amdgcn_readlane(at, src);
   }
-  for (; f < fend; ) {
-  const int len = __builtin_amdgcn_readfirstlane(seq_len(a.lens[seq], cap)), units = units_of(len);
+  while (f < fend) {
+  const int len = len_of(un, a.lens, seq, cap), units = units_of(len);
   if (units == 0) {
     if (++seq == a.batch) {
       seq = 0;
@@ -255,7 +337,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
     }
     continue;
   }
-  const int take = (int)min(fend - f, (int64_t)(begin + units - u));
+  const int take = min(fend - f, begin + units - u);
   const int kbeg = (u - begin) * kUnit, kend = min(len, kbeg + take * kUnit);
 
   // the query heads of this column
@@ -468,13 +550,39 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
     } else {
+      // (agent-scope stores reach the level that all XCDs share)
       float* pp = part_of<D>(a, w, u == begin);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) pp[qh * D + d0 + j] = o[j];
+      for (int j = 0; j < VEC; ++j)
+        __hip_atomic_store(pp + qh * D + d0 + j, o[j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (d0 == 0) {
-        pp[16 * D + 2 * qh] = mj;
-        pp[16 * D + 2 * qh + 1] = lj;
+        __hip_atomic_store(pp + 16 * D + 2 * qh, mj, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(pp + 16 * D + 2 * qh + 1, lj, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+    }
+  }
+  const int f0 = f - (u - begin);
+  const int w0 = share_of(sh, f0), pieces = take == units ? 1 : share_of(sh, f0 + units - 1) - w0 + 1;
+  const int rows = min(16, a.group - first);
+  if (take != units && joined_here(pieces, rows, D)) {
+    // Count the piece at the sequence's counter (that of the workgroup in
+    // whose share it begins: a share holds the beginning of at most one cut
+    // sequence); the last to arrive joins the pieces, in their order, and
+    // clears the counter for the next run.  As in the split products: every
+    // thread's stores are acknowledged before the count (a fence that
+    // releases would write back the XCD's whole L2), and the joining
+    // workgroup acquires at agent scope after it.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+    if (threadIdx.x == 0)
+      last_arrived = __hip_atomic_fetch_add(a.arrivals + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                     (unsigned)(pieces - 1);
+    __syncthreads();
+    if (last_arrived) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      if (threadIdx.x == 0) __hip_atomic_store(a.arrivals + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      join_pieces<T, D>(a, w0, pieces, rows,
+                        (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first) * D, &so[0][0][0]);
     }
   }
   f += take;
@@ -491,13 +599,11 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   }
 }
 
-// Joins the pieces of one sequence and query head, in their order: eight
-// groups of threads take every eighth piece, then add up in LDS.
+// The joins that the main kernel leaves, one workgroup per sequence and query
+// head.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
-  constexpr int LPP = D / 4, GROUPS = 256 / LPP;  // lanes of a piece, pieces at once
-  __shared__ float smax[4], sl[GROUPS];
-  __shared__ f32x4 so[GROUPS][LPP];
+  __shared__ __attribute__((aligned(16))) float lds[256 * 6];
   const int lane = threadIdx.x & 63;
   const int cap = a.width * a.page_size, seq = blockIdx.x, qhead = blockIdx.y;
   const int units = units_of(seq_len(a.lens[seq], cap));
@@ -506,50 +612,22 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
   int at = un.before;
   for (int i = un.i0; i < un.i1 && i < seq; ++i) at += units_of(seq_len(a.lens[i], cap));
   const int begin = __builtin_amdgcn_readlane(at, seq / un.per);
-  const int head = qhead / a.group, qg = qhead % a.group, row = qg % 16;
-  const int columns = a.heads * a.qtiles;
-  const int64_t F = (int64_t)un.total * columns, f0 = (int64_t)un.total * (head * a.qtiles + qg / 16) + begin;
-  const int shares = sharers(F, a.workgroups);
-  const int w0 = share_of(F, f0, shares), count = share_of(F, f0 + units - 1, shares) - w0 + 1;
-  if (count == 1) return;
-  auto piece = [&](int p) { return part_of<D>(a, w0 + p, p == 0); };
-  float m = kNegInf;
-  for (int p = threadIdx.x; p < count; p += 256) m = fmaxf(m, piece(p)[16 * D + 2 * row]);
-  m = wave::all<wave::Max>(m);
-  if (lane == 0) smax[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
-  const float ref = m == kNegInf ? 0.0f : m;
-  const int g = threadIdx.x / LPP, t = threadIdx.x % LPP;
-  f32x4 o = {};
-  float l = 0.0f;
-#pragma unroll 4
-  for (int p = g; p < count; p += GROUPS) {
-    const float* pp = piece(p);
-    const float x = __builtin_amdgcn_exp2f(pp[16 * D + 2 * row] - ref);
-    l += x * pp[16 * D + 2 * row + 1];
-    o += x * *(const f32x4*)(pp + row * D + 4 * t);
-  }
-  so[g][t] = o;
-  if (t == 0) sl[g] = l;
-  __syncthreads();
-  if (g != 0) return;
-  for (int i = 1; i < GROUPS; ++i) {
-    o += so[i][t];
-    l += sl[i];
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T* op = (T*)a.O + seq * a.ldo + (int64_t)qhead * D + 4 * t;
-  *(u32x2*)op = u32x2{pack2_out<T>(o[0] * inv, o[1] * inv), pack2_out<T>(o[2] * inv, o[3] * inv)};
+  const int head = qhead / a.group, qg = qhead % a.group;
+  const Shares sh = make_shares(un.total * a.heads * a.qtiles, a.workgroups);
+  const int f0 = un.total * (head * a.qtiles + qg / 16) + begin;
+  const int w0 = share_of(sh, f0), pieces = share_of(sh, f0 + units - 1) - w0 + 1;
+  if (pieces == 1 || joined_here(pieces, min(16, a.group - qg / 16 * 16), D)) return;
+  join_rows<T, D>(a, w0, pieces, qg % 16, 1, (T*)a.O + seq * a.ldo + (int64_t)qhead * D, lds);
 }
 
-constexpr int kWorkgroups = 512;  // two for each of the 256 CUs
 
 template <typename T, bool FP8, int D>
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((decode_kernel<T, FP8, D>), dim3(a.workgroups), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  const int columns = a.heads * a.qtiles;
+  const int64_t pieces = pieces_bound((int64_t)a.width * a.page_size, columns, a.workgroups);
+  if (e != hipSuccess || joined_here((int)pieces, min(16, a.group), D)) return e;
   hipLaunchKernelGGL((join_kernel<T, D>), dim3(a.batch, a.heads * a.group), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
@@ -607,6 +685,11 @@ bool formats_fit(const gemm_epi_paged_cache* c, gemm_epi_dtype dtype) {
   return (dtype == GEMM_EPI_F16 || dtype == GEMM_EPI_BF16) && (c->dtype == dtype || c->dtype == GEMM_EPI_FP8_E4M3);
 }
 
+// Units of all columns of a full table.
+int64_t units_bound(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
+  return batch * ((width * c->page_size + kUnit - 1) / kUnit) * c->heads * ((q_heads / c->heads + 15) / 16);
+}
+
 struct Shape {
   int group, qtiles, workgroups;
 };
@@ -615,12 +698,13 @@ Shape shape_of(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int6
   s.group = (int)(q_heads / c->heads);
   s.qtiles = (s.group + 15) / 16;
   // no more workgroups than units
-  const int64_t units = batch * ((width * c->page_size + kUnit - 1) / kUnit) * c->heads * s.qtiles;
-  s.workgroups = (int)(units < kWorkgroups ? units : kWorkgroups);
+  const int64_t units = units_bound(c, batch, width, q_heads);
+  const int most = workgroups_for((int)c->head_dim * (c->dtype == GEMM_EPI_FP8_E4M3 ? 1 : 2));
+  s.workgroups = (int)(units < most ? units : most);
   return s;
 }
 size_t workspace_bytes(const gemm_epi_paged_cache* c, int64_t batch, int64_t width, int64_t q_heads) {
-  return (size_t)shape_of(c, batch, width, q_heads).workgroups * 2 * (size_t)(16 * (c->head_dim + 2)) * 4;
+  return kWorkgroups * 4 + (size_t)shape_of(c, batch, width, q_heads).workgroups * 2 * (size_t)(16 * (c->head_dim + 2)) * 4;
 }
 
 template <typename T, bool FP8>
@@ -671,7 +755,8 @@ size_t gemm_epi_attention_decode_workspace_size(const gemm_epi_paged_cache* cach
                                                 int64_t q_heads) {
   using namespace ge::paged;
   if (check_cache(cache, false) != GEMM_EPI_OK || check_sizes(cache->page_size, batch, width) != GEMM_EPI_OK ||
-      q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 16384 || batch == 0)
+      q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 16384 || batch == 0 ||
+      units_bound(cache, batch, width, q_heads) >= kLim)
     return 0;
   return workspace_bytes(cache, batch, width, q_heads);
 }
@@ -685,7 +770,8 @@ gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, con
   if (s == GEMM_EPI_OK) s = check_table(cache, table);
   if (s != GEMM_EPI_OK) return s;
   if (!formats_fit(cache, dtype) || q_heads <= 0 || q_heads % cache->heads != 0) return GEMM_EPI_ERR_INVALID_ARG;
-  if (q_heads > 16384) return GEMM_EPI_ERR_UNSUPPORTED;
+  if (q_heads > 16384 || units_bound(cache, table->batch, table->width, q_heads) >= kLim)
+    return GEMM_EPI_ERR_UNSUPPORTED;
   const int64_t row = q_heads * cache->head_dim;
   if (ldq < row || ldo < row) return GEMM_EPI_ERR_INVALID_ARG;
   if (ldq % 8 != 0 || ldo % 8 != 0) return GEMM_EPI_ERR_UNSUPPORTED;
@@ -703,7 +789,8 @@ gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, con
                      table->lens,
                      Q,
                      O,
-                     (float*)workspace,
+                     (unsigned*)workspace,
+                     (float*)((char*)workspace + kWorkgroups * 4),
                      table->ld,
                      ldq,
                      ldo,

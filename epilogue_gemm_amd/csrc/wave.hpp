@@ -50,5 +50,18 @@ __device__ __forceinline__ float all(float x) {
   return over_rows<Op>(over_row<Op>(x));
 }
 
+// The sum of x over this and all lower lanes (gfx9's scan by DPP: shifts
+// within rows of 16, then the last lane of a row, and of the lower half,
+// added to the rows above).
+__device__ __forceinline__ int scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);  // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);  // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);  // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return x;
+}
+
 }  // namespace wave
 }  // namespace ge

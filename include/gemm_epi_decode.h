@@ -161,6 +161,8 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
                                       const void* K, int64_t ldk, const void* V, int64_t ldv, const int32_t* starts,
                                       int64_t tokens, gemm_epi_dtype dtype, void* stream);
 
+#define GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES 2048
+
 /* gemm_epi_attention_decode -- attention of one new token of each sequence
  * over its cache,
  *
@@ -179,16 +181,20 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
  * remainder); O is rounded once.  The keys are split over workgroups by the
  * lengths found on the device and joined in a fixed order: the same inputs
  * give the same bits.
- * workspace: gemm_epi_attention_decode_workspace_size bytes, 16-byte aligned,
- * with no content of its own before or after a call; runs that share it must
+ * workspace: gemm_epi_attention_decode_workspace_size bytes, 16-byte aligned.
+ * Its first GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES hold counters: zero-filled
+ * once before its first use, and left zero by every run that completes; the
+ * rest has no content of its own before or after a call.  One workspace
+ * serves calls of any sizes it is large enough for; runs that share it must
  * not overlap in time.
  * batch = 0 does nothing.
  * Errors: INVALID_ARG (a NULL pointer, a negative or zero size, q_heads not a
  * multiple of the cache's heads, an ld below its minimum, formats that do
  * not fit, workspace missing or too small),
  * UNSUPPORTED (the cache's and table's limits of gemm_epi_cache_append; Q, O
- * or workspace not 16-byte aligned, ldq or ldo not a multiple of 8, more than 16384 query
- * heads), HIP. */
+ * or workspace not 16-byte aligned, ldq or ldo not a multiple of 8, more than
+ * 16384 query heads, batch times the 128-token units of width * page_size
+ * times heads times the tiles of 16 query heads of a key head >= 2^31), HIP. */
 gemm_epi_status gemm_epi_attention_decode(const gemm_epi_paged_cache* cache, const gemm_epi_page_table* table,
                                           const void* Q, int64_t ldq, void* O, int64_t ldo, int64_t q_heads,
                                           gemm_epi_dtype dtype, void* workspace, size_t workspace_bytes,

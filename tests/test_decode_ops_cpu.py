@@ -200,9 +200,11 @@ int c_divide(int n, int d) { return divide(n, make_divider(d)); }
 int64_t c_row_of(int p, int hs, int h, int ps, int s) { return row_of(p, hs, h, ps, s); }
 int c_new_position(int len, int end, int row, int cap) { return new_position(len, end, row, cap); }
 int c_units_of(int len) { return units_of(len); }
-int c_sharers(int64_t F, int n) { return sharers(F, n); }
-int64_t c_share_begin(int64_t F, int w, int n) { return share_begin(F, w, n); }
-int c_share_of(int64_t F, int64_t f, int n) { return share_of(F, f, n); }
+int c_shares(int F, int n) { return make_shares(F, n).n; }
+int c_share_begin(int F, int n, int w) { return share_begin(make_shares(F, n), w); }
+int c_share_of(int F, int n, int f) { return share_of(make_shares(F, n), f); }
+int c_joined_here(int pieces, int rows, int d) { return joined_here(pieces, rows, d); }
+int64_t c_pieces_bound(int64_t cap, int columns, int n) { return pieces_bound(cap, columns, n); }
 }
 '''
 
@@ -218,10 +220,8 @@ def paged(tmp_path_factory):
     assert r.returncode == 0, r.stderr
     lib = ctypes.CDLL(str(so))
     lib.c_row_of.restype = ctypes.c_int64
-    lib.c_share_begin.restype = ctypes.c_int64
-    lib.c_share_begin.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
-    lib.c_sharers.argtypes = [ctypes.c_int64, ctypes.c_int]
-    lib.c_share_of.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+    lib.c_pieces_bound.restype = ctypes.c_int64
+    lib.c_pieces_bound.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
     return lib
 
 
@@ -268,14 +268,42 @@ def test_units(paged):
 @pytest.mark.parametrize("seed", range(40))
 def test_shares_cover_every_unit_once(paged, seed):
     rng = np.random.default_rng(seed)
-    F = int(rng.choice([1, 2, 7, 511, 512, 513, 100003, 1 << 31, (1 << 31) * 2048 - 5]))
-    given = int(rng.choice([1, 2, 8, 63, 512, 1024]))
-    W = paged.c_sharers(F, given)
-    assert W == min(F, given)
-    begins = [paged.c_share_begin(F, w, W) for w in range(W + 1)]
+    F = int(rng.choice([1, 2, 7, 511, 512, 513, 100003, 1 << 30, INT_MAX]))
+    given = int(rng.choice([1, 2, 8, 63, 512]))
+    W = paged.c_shares(F, given)
+    assert W == min(F, given) and paged.c_shares(0, given) == 0
+    begins = [paged.c_share_begin(F, given, w) for w in range(W + 1)]
     assert begins[0] == 0 and begins[-1] == F
-    sizes = np.diff(begins)
+    sizes = np.diff(np.array(begins, dtype=np.int64))
     assert sizes.min() >= 1 and sizes.max() - sizes.min() <= 1  # even
     for f in {0, F - 1, *[int(x) for x in rng.integers(0, F, 50)], *[b for b in begins if b < F], *[b - 1 for b in begins if b > 0]}:
-        w = paged.c_share_of(F, f, W)
+        w = paged.c_share_of(F, given, f)
         assert begins[w] <= f < begins[w + 1], (F, W, f)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_pieces_stay_within_their_bound(paged, seed):
+    # a batch's sequences, column by column, cut where shares end
+    rng = np.random.default_rng(100 + seed)
+    cap = int(rng.choice([16, 128, 1000, 8192, 100000]))
+    units = [paged.c_units_of(int(n)) for n in rng.integers(0, cap + 1, size=int(rng.integers(1, 40)))]
+    columns, given = int(rng.choice([1, 2, 8, 30, 600])), 512
+    F = sum(units) * columns
+    bound = paged.c_pieces_bound(cap, columns, given)
+    at = 0
+    for _ in range(min(columns, 3)):
+        for u in units:
+            if u:
+                pieces = paged.c_share_of(F, given, at + u - 1) - paged.c_share_of(F, given, at) + 1
+                assert pieces <= bound, (pieces, bound)
+            at += u
+
+
+def test_who_joins(paged):
+    # more pieces or rows never move a join into the main kernel
+    for d in (64, 128):
+        for rows in range(1, 17):
+            here = [paged.c_joined_here(p, rows, d) for p in range(1, 600)]
+            assert here[0] and here == sorted(here, reverse=True)
+            if rows > 1:
+                assert all(a <= b for a, b in zip(here, [paged.c_joined_here(p, rows - 1, d) for p in range(1, 600)]))

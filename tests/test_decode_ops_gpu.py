@@ -413,6 +413,7 @@ def attend(pool, q, extra=0, ws="own"):
     if ws == "dirty":
         n = pool.cache.workspace_size(q.shape[1], pages)
         workspace = torch.full((n // 4,), NAN, device="cuda")
+        workspace[:gb.ATTENTION_DECODE_COUNTER_BYTES // 4] = 0
     pool.cache.attend(qd, o, pages, pool.lens.cuda(), workspace=workspace)
     torch.cuda.synchronize()
     if extra:
@@ -448,6 +449,25 @@ def test_attend_strides_and_dirty_workspace(head_dim, dtype, cache):
     first = attend(pool, q, extra=24, ws="dirty")
     within(first, want, tol, "strided")
     assert torch.equal(first, attend(pool, q, extra=8, ws="dirty")), "same inputs, other bits"
+
+
+def test_attend_one_workspace_for_calls_of_any_sizes():
+    # large and small calls in turn on one workspace: its counters are zero
+    # after each, whatever the call before left behind them
+    pools = [Pool(LENS[n], 2, d, 16, "bf16", "bf16", 70) for n, d in (("long", 128), ("mixed", 64), ("one", 128), ("many", 64))]
+    need = 0
+    for p in pools:
+        p.fill(71)
+        need = max(need, p.cache.workspace_size(6, p.table))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for p in pools + pools[::-1]:
+        q = rand(gen(72), p.table.shape[0], 6, p.head_dim)
+        want, tol = attend_want(p, q)
+        o = torch.full_like(q, NAN, device="cuda")
+        p.cache.attend(q.cuda(), o, p.table.cuda(), p.lens.cuda(), workspace=ws)
+        torch.cuda.synchronize()
+        within(o, want, tol, "one workspace")
+        assert int(ws[:gb.ATTENTION_DECODE_COUNTER_BYTES].count_nonzero()) == 0
 
 
 def test_attend_missing_pages():
@@ -660,7 +680,7 @@ class Step:
         e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
         self.x, self.res = rand(g, B, K).cuda(), rand(g, B, K).cuda()
         self.h, self.y, self.delta, self.qkv, self.o, self.out = e(B, K), e(B, K), e(B, N), e(B, N), e(B, self.hq, self.D), e(B, K)
-        self.ws = torch.empty(self.pool.cache.workspace_size(self.hq, self.pages), dtype=torch.uint8, device="cuda")
+        self.ws = torch.zeros(self.pool.cache.workspace_size(self.hq, self.pages), dtype=torch.uint8, device="cuda")
         self.lws = torch.empty(gb.lora_workspace_size(B, N, K, 16, 3), dtype=torch.uint8, device="cuda")
         self.p_qkv = gb.Plan(B, N, K, "bf16", "bf16", "row", "col", "bias")
         self.p_out = gb.Plan(B, K, self.hq * self.D, "bf16", "bf16", "row", "col", "bias")
@@ -751,7 +771,7 @@ def test_two_streams_at_once():
         tabs.append(p.table.cuda())
         lens.append(p.lens.cuda())
         os_.append(torch.empty(3, 8, 128, dtype=torch.bfloat16, device="cuda"))
-        wss.append(torch.empty(p.cache.workspace_size(8, tabs[i]), dtype=torch.uint8, device="cuda"))
+        wss.append(torch.zeros(p.cache.workspace_size(8, tabs[i]), dtype=torch.uint8, device="cuda"))
     qd = [q.cuda() for q in qs]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
