@@ -2,13 +2,16 @@
 //
 //     C[m] = R[m] + s[a] (X[m] A[a]^T) B[a]^T        a = ids[m]
 //
-// Two kernels.  `shrink` forms U = X A^T (rank values a row) as fp32 partial
-// sums over ranges of K; `expand` adds the partials in their order, brings
-// U to the input format in two parts and multiplies with B.  Rows come in
-// any order of adapters: a workgroup takes 16 or 32 consecutive rows -- MFMA
-// operands -- and runs once over each adapter that occurs among them, keeping
-// of each product the rows that are the adapter's.  Few rows: the adapters
-// of a tile are spread over workgroups (grid z), K over more ranges.
+// Two kernels.  `shrink` forms the inner products U = X A^T (rank values a
+// row) as fp32 partial sums over ranges of K; `expand` adds the partials in
+// their order, brings U to the input format in two parts and does the second
+// product for a range of columns.  Rows come in any order of adapters: a
+// workgroup takes 16 or 32 consecutive rows -- MFMA operands -- and runs once
+// over each adapter that occurs among them, keeping of each product the rows
+// that are the adapter's; where rows are few, the adapters of a tile are
+// spread over workgroups (grid z).  (Both products in one kernel, U never
+// leaving LDS, was measured slower everywhere: 4096 x 4096 -> 4096, rank 64,
+// 48 us against 38, as a tile's A and B then pass through one CU.)
 #include "gemm_tile16.hpp"
 #include "wave.hpp"
 
@@ -52,105 +55,344 @@ __device__ __forceinline__ void each_adapter(const Args& a, int row0, int lane, 
   }
 }
 
-// U^T = A X^T: first operand 16 of the adapter's rows, second 16 rows of X,
-// so that lane (m = l % 16, h = l / 16) receives U[m][16 t + 4 h + e].
-// Workgroup (tile, range, z) takes the adapters number z, z + Z, ... of its
-// rows; its NW waves take every NW-th 32-deep step and add up in LDS.
-// Bound by X (and, for few rows, the adapters) from memory: UNR steps' loads
-// are in flight together.
+// Bytes of LDS a wave stages its operands and results in.
+template <int RT, int MT>
+constexpr int wave_bytes() {
+  const int first = (MT + RT) * 2048, second = 64 * (16 * RT + 8) * 2, out = 16 * 68 * 4;
+  return first > second ? (first > out ? first : out) : (second > out ? second : out);
+}
+
+// U^T += A X^T over one of NW waves' part of [kbeg, kend): first operand 16 of
+// the adapter's rows, second 16 rows of X, so that lane (m = l % 16, h = l /
+// 16) receives U[m][16 t + 4 h + e].  A wave's part is contiguous and taken
+// in stages of 64 columns.  Loads take whole cache lines, eight rows of 128
+// bytes an instruction (sixteen half lines, an operand's own shape, cost the
+// L1 twice as long), and change lanes through the wave's own LDS: 16-byte
+// chunk x of row r at x ^ (r / 2 % 8), which keeps an operand's 16 rows on
+// different banks.  The next stage's loads are in flight while one is
+// multiplied.  The waves' parts and the tiles' first stages (`turn`) lie
+// apart, for the memory channels' sake.
 template <typename T, int RT, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void shrink(Args a) {
-  constexpr int RP = 16 * RT, ROWS = 16 * MT, UNR = RT + MT > 8 ? 1 : RT + MT > 3 ? 2 : 4;
-  __shared__ float red[NW][ROWS][RP + 1];
+__device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[MT][RT], int row0, int ad, int kbeg, int kend, char* lds,
+                                      int wave, int lane, int turn) {
+  const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
+  const T* x[MT][2];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      x[i][j] = (const T*)a.X + (int64_t)min(row0 + 16 * i + 8 * j + lr, a.M - 1) * a.ldx + 8 * lc;
+  const T* ab = (const T*)a.A + (int64_t)ad * a.rank * a.K;
+  const uint32_t aoff = (uint32_t)lr * a.K + 8 * lc;
+  const int part = (kend - kbeg + 64 * NW - 1) / (64 * NW) * 64;
+  const int k1 = kbeg + part * wave, k2 = min(kend, k1 + part);
+  const int stages = k2 > k1 ? (k2 - k1 + 63) / 64 : 0;
+  if (stages == 0) return;
+  u32x4 g[MT + RT][2];
+  bool in;  // this lane's columns of the stage exist (K is a multiple of 8)
+  int at = turn % stages;
+  auto load = [&]() __attribute__((always_inline)) {
+    const int k0 = k1 + 64 * at;
+    if (++at == stages) at = 0;
+    in = k0 + 8 * lc < k2;
+    const int k = in ? k0 : -8 * lc;  // (else the row's first: a valid address)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) g[i][j] = *(const u32x4*)(x[i][j] + k);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        // eight rows exist or not together, as the rank is a multiple of 8
+        const int r = 16 * t + 8 * j < a.rank ? 16 * t + 8 * j : 0;
+        g[MT + t][j] = *(const u32x4*)(ab + (int64_t)r * a.K + (int64_t)k + aoff);
+      }
+    }
+  };
+  char* const w = lds + lr * 128 + ((lc ^ (lr >> 1)) << 4);
+  char* const w1 = lds + (8 + lr) * 128 + ((lc ^ (4 + (lr >> 1))) << 4);
+  const char* const rd = lds + c * 128;
+  load();
+  for (int n = 0; n < stages; ++n) {
+    if (__builtin_amdgcn_ballot_w64(!in)) {
+#pragma unroll
+      for (int t = 0; t < MT + RT; ++t)
+        if (!in) g[t][0] = g[t][1] = u32x4{};
+    }
+#pragma unroll
+    for (int t = 0; t < MT + RT; ++t) {
+      *(u32x4*)(w + 2048 * t) = g[t][0];
+      *(u32x4*)(w1 + 2048 * t) = g[t][1];
+    }
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses are done in order)
+    load();                           // (past the last stage: the first again)
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int chunk = ((4 * s + h) ^ (c >> 1)) << 4;
+      u32x4 xf[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xf[i] = *(const u32x4*)(rd + 2048 * i + chunk);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const u32x4 af = *(const u32x4*)(rd + 2048 * (MT + t) + chunk);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][t] = mfma16<T>(af, xf[i], acc[i][t]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Eight values of a row of U, whose other pieces are in the next PIECES - 1
+// lanes, in two 16-bit parts: scaled by 2^-ex, which brings the row's largest
+// value into [1/2, 1), the rounded value and its rounded remainder (U's error
+// is the result's).  Returns ex.
+template <typename T, int PIECES>
+__device__ __forceinline__ int split(const float (&u)[8], u32x4& hi, u32x4& lo) {
+  float mx = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(u[e]));
+#pragma unroll
+  for (int d = 1; d < PIECES; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  // (an infinite or zero row is left as it is)
+  const int ex = mx > 0.0f && mx < __builtin_inff() ? max(__builtin_amdgcn_frexp_expf(mx), -120) : 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float v0 = __builtin_amdgcn_ldexpf(u[2 * e], -ex), v1 = __builtin_amdgcn_ldexpf(u[2 * e + 1], -ex);
+    const T t0 = from_f32<T>(v0), t1 = from_f32<T>(v1);
+    hi[e] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
+    // (the remainder of an infinity is no number: it has none)
+    lo[e] = pack2_out<T>(fabsf(v0) < __builtin_inff() ? v0 - to_f32(t0) : 0.0f,
+                         fabsf(v1) < __builtin_inff() ? v1 - to_f32(t1) : 0.0f);
+  }
+  return ex;
+}
+
+// The second product of a wave, C^T = B U^T, for every column n0 + step i, 64
+// columns at a time: first operand 16 rows of B (columns of C), second 16
+// rows of U, so that lane (m, h) receives four columns of row m per product;
+// once for each adapter of list[0 .. count), keeping the rows that are the
+// adapter's.  The 64 rows of B are contiguous and loaded so, then change
+// lanes through the wave's LDS (rows of RP + 8 values, those past the rank
+// zero); C's 16 x 64 change lanes there too, so that R and C move in whole
+// lines, eight rows of 128 bytes an instruction.  The next turn's B and R
+// two turns on are in flight while one is multiplied.  Only the rows of `mine` are written.
+template <typename T, int RT, int MT, bool PAST>
+__device__ __forceinline__ void second(const Args& a, int row0, int n0, int step, const int* list, int count, uint32_t mine,
+                                       const uint16_t (&su)[2][16 * MT][16 * RT + 8], const int* sex, char* lds, int lane) {
+  constexpr int RP = 16 * RT, ST = (RP + 31) / 32, LD = RP + 8, BL = 2 * RT;
+  if (n0 >= a.N) return;
+  const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
+  int id[MT], ex[MT];
+  float back[MT];
+  u32x4 uh[MT][ST], ul[MT][ST];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    id[i] = row_adapter(a, row0 + 16 * i + c);
+    ex[i] = id[i] < 0 ? 0 : sex[16 * i + c];
+    back[i] = id[i] < 0 ? 0.0f : a.scale ? a.scale[id[i]] : 1.0f;
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
+      const int r = 32 * s + 8 * h;
+      // (rows without an adapter have no U)
+      uh[i][s] = r < RP && id[i] >= 0 ? *(const u32x4*)&su[0][16 * i + c][r] : u32x4{};
+      ul[i][s] = r < RP && id[i] >= 0 ? *(const u32x4*)&su[1][16 * i + c][r] : u32x4{};
+    }
+  }
+  // this lane's 16-byte pieces of 64 rows of B, and where they go in LDS
+  const int pieces = a.rank >> 3;  // of a row; lane + 64 i < 64 pieces for i < pieces
+  int dst[BL];
+#pragma unroll
+  for (int i = 0; i < BL; ++i) {
+    const int q = lane + 64 * i;
+    dst[i] = (q / pieces * LD + q % pieces * 8) * 2;
+  }
+  auto load_b = [&](u32x4(&b)[BL], int ad, int n) __attribute__((always_inline)) {
+    const T* p = (const T*)a.B + ((int64_t)ad * a.N + n) * a.rank;
+    const int most = min(64, a.N - n) * pieces - 1;
+#pragma unroll
+    for (int i = 0; i < BL; ++i)
+      if (i < pieces) b[i] = *(const u32x4*)(p + 8 * min(lane + 64 * i, most));
+  };
+  auto load_r = [&](u32x4(&r)[MT][2], int n) __attribute__((always_inline)) {
+    if (!a.vec || !a.R || n + 64 > a.N) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const T* p = (const T*)a.R + (int64_t)min(row0 + 16 * i + 8 * j + lr, a.M - 1) * a.ldr + n + 8 * lc;
+        r[i][j] = PAST ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p;
+      }
+  };
+  // C for the 64 columns from n on
+  auto store = [&](const f32x4(&out)[MT][4], const u32x4(&r)[MT][2], int n) __attribute__((always_inline)) {
+    const bool vec = a.vec && n + 64 <= a.N;
+    float* const f = (float*)lds;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = id[i] < 0 ? 0.0f : __builtin_amdgcn_ldexpf(out[i][j][e], ex[i]) * back[i];
+        *(f32x4*)(f + c * 68 + 16 * j + 4 * h) = v;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = 16 * i + 8 * j + lr, row = row0 + m, at = n + 8 * lc;
+        const f32x4 v0 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc), v1 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc + 4);
+        float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+        if (row >= a.M || !(mine >> m & 1)) continue;
+        T* cp = (T*)a.C + (int64_t)row * a.ldc + at;
+        if (vec) {
+          if (a.R) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[2 * e] += to_f32(__builtin_bit_cast(T, (uint16_t)(r[i][j][e] & 0xffffu)));
+              v[2 * e + 1] += to_f32(__builtin_bit_cast(T, (uint16_t)(r[i][j][e] >> 16)));
+            }
+          }
+          u32x4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack2_out<T>(v[2 * e], v[2 * e + 1]);
+          if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4*)cp);
+          else *(u32x4*)cp = w;
+        } else {
+          const T* rp = a.R ? (const T*)a.R + (int64_t)row * a.ldr + at : nullptr;
+          for (int e = 0; e < 8; ++e)
+            if (at + e < a.N) cp[e] = from_f32<T>(v[e] + (rp ? to_f32(rp[e]) : 0.0f));
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+  f32x4 out[MT][4] = {};
+  u32x4 r0[MT][2], r1[MT][2], r2[MT][2];
+  if (count == 0) {  // no adapter: C = R
+    for (; n0 < a.N; n0 += step) {
+      load_r(r0, n0);
+      store(out, r0, n0);
+    }
+    return;
+  }
+  // the turns: each adapter for 64 columns, then the next 64
+  u32x4 b[BL];
+  int k = 0;
+  load_b(b, __builtin_amdgcn_readfirstlane(list[0]), n0);
+  load_r(r0, n0);
+  load_r(r1, n0 + step < a.N ? n0 + step : n0);
+  const char* const rd = lds + 16 * h;
+  for (;;) {
+    const int ad = __builtin_amdgcn_readfirstlane(list[k]);
+    // B to LDS; columns past the rank are zero
+#pragma unroll
+    for (int i = 0; i < BL; ++i)
+      if (i < pieces) *(u32x4*)(lds + dst[i]) = b[i];
+    if (a.rank < 32 * ST)
+      for (int i = a.rank; i < 32 * ST && i < LD; i += 8) *(u32x4*)(lds + (lane * LD + i) * 2) = u32x4{};
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses are done in order)
+    // the next turn's loads (past the last: this one's again)
+    const int kn = k + 1 == count ? 0 : k + 1, nn = kn == 0 ? n0 + step : n0;
+    const bool more = nn < a.N;
+    load_b(b, __builtin_amdgcn_readfirstlane(list[kn]), more ? nn : n0);
+    if (kn == 0) load_r(r2, nn + step < a.N ? nn + step : n0);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 bf[ST];
+#pragma unroll
+      for (int s = 0; s < ST; ++s)
+        bf[s] = 32 * s + 8 * h < LD ? *(const u32x4*)(rd + ((16 * j + c) * LD + 32 * s) * 2) : u32x4{};
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        f32x4 acc = {};
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+          acc = mfma16<T>(bf[s], uh[i][s], acc);
+          acc = mfma16<T>(bf[s], ul[i][s], acc);
+        }
+        if (id[i] == ad) out[i][j] = acc;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (kn == 0) {
+      store(out, r0, n0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        r0[i][0] = r1[i][0];
+        r0[i][1] = r1[i][1];
+        r1[i][0] = r2[i][0];
+        r1[i][1] = r2[i][1];
+      }
+    }
+    if (!more) return;
+    n0 = nn;
+    k = kn;
+  }
+}
+
+// U's partial sums.  Workgroup (tile, range, z) takes the adapters number z, z
+// + Z, ... of its 16 MT rows; its four waves add up in LDS.
+template <typename T, int RT, int MT>
+__global__ __launch_bounds__(256) void shrink(Args a) {
+  constexpr int RP = 16 * RT, ROWS = 16 * MT, PER = wave_bytes<RT, MT>();
+  static_assert(ROWS * (RP + 1) * 4 <= PER, "a wave's sums take the place of its operands");
+  __shared__ __attribute__((aligned(16))) char lds[4 * PER];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
   const int row0 = blockIdx.x * ROWS;
-  const T* x[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) x[i] = (const T*)a.X + (int64_t)min(row0 + 16 * i + c, a.M - 1) * a.ldx + 8 * h;
   const int kbeg = blockIdx.y * a.kper, kend = min(a.K, kbeg + a.kper);
   uint32_t number = 0;
   each_adapter<MT>(a, row0, lane, [&](int ad, uint32_t rows) {
     if (number++ % gridDim.z != blockIdx.z) return;
-    const T* ar[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      ar[t] = (const T*)a.A + ((int64_t)ad * a.rank + min(16 * t + c, a.rank - 1)) * a.K + 8 * h;
     f32x4 acc[MT][RT] = {};
-    int k0 = kbeg + 32 * wave;
-    for (; k0 + 32 * NW * (UNR - 1) + 32 <= kend; k0 += 32 * NW * UNR) {
-      u32x4 xf[UNR][MT], af[UNR][RT];
-#pragma unroll
-      for (int n = 0; n < UNR; ++n) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) xf[n][i] = *(const u32x4*)(x[i] + k0 + 32 * NW * n);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) af[n][t] = *(const u32x4*)(ar[t] + k0 + 32 * NW * n);
-      }
-#pragma unroll
-      for (int n = 0; n < UNR; ++n)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) acc[i][t] = mfma16<T>(af[n][t], xf[n][i], acc[i][t]);
-    }
-    for (; k0 < kend; k0 += 32 * NW) {
-      const bool in = k0 + 8 * h < kend;
-      u32x4 xf[MT], af[RT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xf[i] = in ? *(const u32x4*)(x[i] + k0) : u32x4{};
-#pragma unroll
-      for (int t = 0; t < RT; ++t) af[t] = in ? *(const u32x4*)(ar[t] + k0) : u32x4{};
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[i][t] = mfma16<T>(af[t], xf[i], acc[i][t]);
-    }
-    __syncthreads();  // the last adapter's sums have been read
+    inner<T, RT, MT, 4>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
+    __syncthreads();  // every wave has read its operands: their place holds the sums
+    float* red = (float*)(lds + wave * PER);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][16 * i + c][16 * t + 4 * h + e] = acc[i][t][e];
+        for (int e = 0; e < 4; ++e) red[(16 * i + c) * (RP + 1) + 16 * t + 4 * h + e] = acc[i][t][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < ROWS * RP; i += 64 * NW) {
+    for (int i = threadIdx.x; i < ROWS * RP; i += 256) {
       const int m = i / RP, r = i % RP;
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += red[w][m][r];
+      for (int w = 0; w < 4; ++w) sum += ((const float*)(lds + w * PER))[m * (RP + 1) + r];
       if (rows >> m & 1) a.U[((int64_t)blockIdx.y * a.M + row0 + m) * RP + r] = sum;
     }
+    __syncthreads();  // the sums have been read
   });
 }
 
-// C^T = B U^T: first operand 16 rows of B (columns of C), second 16 rows of
-// U, so that lane (m, h) receives four columns of row m per product.  The
-// rows of B are fed to the four products of a wave's 64 columns so that a
-// lane has columns 32 p + 8 h .. + 7 (p = 0, 1): 16-byte pieces of R and C.
-// The workgroup first adds up its rows' partials, eight values a thread, and
-// leaves U in LDS in two 16-bit parts: scaled by a power of two that brings
-// its row's largest value into [1/2, 1), the rounded value and its rounded
-// remainder (U's error is the result's).  Then each wave takes every fourth
-// 64 columns of the workgroup's.  Bound by R and C (for few rows: by B), U
-// and B being small or in the caches.
-template <typename T, int RT, int MT>
+// The second product.  The workgroup adds up its rows' partials, eight values
+// a thread, leaves U's two parts in LDS, and each wave takes every fourth 64
+// columns of the workgroup's.  PAST: R and C are more than the caches hold and
+// move past them.
+template <typename T, int RT, int MT, bool PAST>
 __global__ __launch_bounds__(256) void expand(Args a) {
-  constexpr int RP = 16 * RT, ST = (RP + 31) / 32, ROWS = 16 * MT;
-  constexpr int PIECES = RP / 8, LD = RP + 8;  // of a row; a row in LDS
-  __shared__ __attribute__((aligned(16))) uint16_t su[2][ROWS][LD];
-  __shared__ int sex[ROWS];
+  constexpr int RP = 16 * RT, ROWS = 16 * MT, PIECES = RP / 8, PER = wave_bytes<RT, MT>();
+  __shared__ __attribute__((aligned(16))) char lds[4 * PER];
+  __shared__ __attribute__((aligned(16))) uint16_t su[2][ROWS][RP + 8];
+  __shared__ int sex[ROWS], list[ROWS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, h = lane >> 4;
   const int row0 = blockIdx.x * ROWS;
   // the rows of the adapters that are this workgroup's; those without one are
   // the first workgroup's
   uint32_t mine = 0;
+  int count = 0;
   {
     uint32_t number = 0, some = 0;
-    each_adapter<MT>(a, row0, lane, [&](int, uint32_t rows) {
+    each_adapter<MT>(a, row0, lane, [&](int ad, uint32_t rows) {
       some |= rows;
-      if (number++ % gridDim.z == blockIdx.z) mine |= rows;
+      if (number++ % gridDim.z == blockIdx.z) {
+        mine |= rows;
+        if (threadIdx.x == 0) list[count] = ad;
+        ++count;
+      }
     });
     if (mine == 0 && blockIdx.z != 0) return;
     if (blockIdx.z == 0) mine |= ~some;
@@ -173,152 +415,66 @@ __global__ __launch_bounds__(256) void expand(Args a) {
         }
       }
     }
-    float mx = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(u[e]));
-#pragma unroll
-    for (int d = 1; d < PIECES; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    // (an infinite or zero row is left as it is)
-    const int ex = mx > 0.0f && mx < __builtin_inff() ? max(__builtin_amdgcn_frexp_expf(mx), -120) : 0;
     u32x4 hi, lo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v0 = __builtin_amdgcn_ldexpf(u[2 * e], -ex), v1 = __builtin_amdgcn_ldexpf(u[2 * e + 1], -ex);
-      const T t0 = from_f32<T>(v0), t1 = from_f32<T>(v1);
-      hi[e] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
-      // (the remainder of an infinity is no number: it has none)
-      lo[e] = pack2_out<T>(fabsf(v0) < __builtin_inff() ? v0 - to_f32(t0) : 0.0f,
-                           fabsf(v1) < __builtin_inff() ? v1 - to_f32(t1) : 0.0f);
-    }
+    const int ex = split<T, PIECES>(u, hi, lo);
     *(u32x4*)&su[0][m][r] = hi;
     *(u32x4*)&su[1][m][r] = lo;
     if (r == 0) sex[m] = ex;
   }
   __syncthreads();
-  int id[MT], ex[MT];
-  u32x4 uh[MT][ST], ul[MT][ST];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    id[i] = row_adapter(a, row0 + 16 * i + c);
-    ex[i] = sex[16 * i + c];
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      const int r = 32 * s + 8 * h;
-      uh[i][s] = r < RP ? *(const u32x4*)&su[0][16 * i + c][r] : u32x4{};
-      ul[i][s] = r < RP ? *(const u32x4*)&su[1][16 * i + c][r] : u32x4{};
-    }
-  }
-  for (int n0 = (blockIdx.y * 4 + wave) * 64; n0 < a.N; n0 += gridDim.y * 256) {
-    // R's pieces first: nothing depends on them until the end
-    u32x4 rr[MT][2];
-    const bool vec = a.vec && n0 + 64 <= a.N;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        rr[i][p] = vec && a.R && row0 + 16 * i + c < a.M
-                       ? *(const u32x4*)((const T*)a.R + (int64_t)(row0 + 16 * i + c) * a.ldr + n0 + 32 * p + 8 * h)
-                       : u32x4{};
-    f32x4 out[MT][4] = {};
-    each_adapter<MT>(a, row0, lane, [&](int ad, uint32_t rows) {
-      if ((rows & mine) == 0) return;
-      const T* b = (const T*)a.B + (int64_t)ad * a.N * a.rank;
-      u32x4 bf[4][ST];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = min(n0 + 32 * (j >> 1) + 8 * (c >> 2) + 4 * (j & 1) + (c & 3), a.N - 1);
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          const int r = 32 * s + 8 * h;
-          bf[j][s] = r < a.rank ? *(const u32x4*)(b + (int64_t)n * a.rank + r) : u32x4{};
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f32x4 acc = {};
-#pragma unroll
-          for (int s = 0; s < ST; ++s) {
-            acc = mfma16<T>(bf[j][s], uh[i][s], acc);
-            acc = mfma16<T>(bf[j][s], ul[i][s], acc);
-          }
-          if (id[i] == ad) out[i][j] = acc;
-        }
-    });
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int row = row0 + 16 * i + c;
-      if (row >= a.M || !(mine >> (16 * i + c) & 1)) continue;
-      const float back = id[i] >= 0 && a.scale ? a.scale[id[i]] : 1.0f;
-      T* cp = (T*)a.C + (int64_t)row * a.ldc;
-      const T* rp = a.R ? (const T*)a.R + (int64_t)row * a.ldr : nullptr;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = n0 + 32 * p + 8 * h;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = id[i] < 0 ? 0.0f : __builtin_amdgcn_ldexpf(out[i][2 * p + (e >> 2)][e & 3], ex[i]) * back;
-        if (vec) {
-          u32x4 w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float r0 = to_f32(__builtin_bit_cast(T, (uint16_t)(rr[i][p][e] & 0xffffu)));
-            const float r1 = to_f32(__builtin_bit_cast(T, (uint16_t)(rr[i][p][e] >> 16)));
-            w[e] = pack2_out<T>(v[2 * e] + r0, v[2 * e + 1] + r1);
-          }
-          *(u32x4*)(cp + n) = w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < a.N) cp[n + e] = from_f32<T>(v[e] + (rp ? to_f32(rp[n + e]) : 0.0f));
-        }
-      }
-    }
-  }
+  second<T, RT, MT, PAST>(a, row0, (blockIdx.y * 4 + wave) * 64, gridDim.y * 256, list, count, mine, su, sex, lds + wave * PER, lane);
 }
 
-// How a problem is cut, by its sizes alone.  Many rows (from 1024): 32 of
-// them share an adapter's values (MT = 2), eight waves add up a range.
+// How a problem is cut, by its sizes alone.
 struct Cut {
-  int mt, nw, tiles, ksplit, kper;
+  int mt, tiles;     // tiles of 16 mt rows
+  int ksplit, kper;  // ranges of K
 };
-inline Cut cut(int64_t M, int64_t K) {
+inline Cut cut(int64_t M, int64_t K, int64_t rank) {
   Cut s;
-  s.mt = M >= 1024 ? 2 : 1;
-  s.nw = 4 * s.mt;
+  // 32 rows share an adapter's values where there are tiles enough (16384
+  // rows, rank 64: 122 us against 139)
+  s.mt = M >= 8192 && rank <= 64 ? 2 : 1;
   s.tiles = (int)((M + 16 * s.mt - 1) / (16 * s.mt));
-  // ranges of K: some 256 workgroups, two steps of its waves or more each
-  const int step = 32 * s.nw;
+  // ranges of K: some 256 workgroups, one stage of their waves or more each
   int64_t ks = s.tiles >= 256 ? 1 : 256 / s.tiles;
-  const int64_t most = (K + 2 * step - 1) / (2 * step);
+  const int64_t most = (K + 255) / 256;
   if (ks > most) ks = most;
-  s.kper = (int)(((K + ks - 1) / ks + step - 1) / step * step);
+  s.kper = (int)(((K + ks - 1) / ks + 255) / 256 * 256);
   s.ksplit = (int)((K + s.kper - 1) / s.kper);
   return s;
 }
 
 inline int64_t rank_pad(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
+// Workgroups among which a tile's adapters are spread (grid z): as many as it
+// can hold where tiles are few.  Those that find no adapter of theirs end at
+// once; `expand`, whose rows cost more than its adapters, spreads less.
 template <typename T, int RT, int MT>
 hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
-  // workgroups among which a tile's adapters are spread: as many as it can
-  // hold where tiles are few
-  const int z = min(min(a.adapters, a.M), s.tiles <= 4 ? 16 : s.tiles <= 256 ? 4 : 1);
-  // columns of a workgroup: 256 each, or more where that still leaves 512
-  // workgroups, so that U is read and split less often
-  const int chunks = (a.N + 255) / 256, y = min(chunks, max(1, 512 / s.tiles));
-  hipLaunchKernelGGL((shrink<T, RT, MT, 4 * MT>), dim3(s.tiles, s.ksplit, z), dim3(256 * MT), 0, stream, a);
+  const int most = min(a.adapters, min(a.M, 16));
+  const int zs = s.tiles <= 4 ? most : s.tiles <= 256 ? min(most, 4) : 1;
+  const int ze = s.tiles <= 4 ? most : s.tiles <= 32 ? min(most, 4) : 1;
+  hipLaunchKernelGGL((shrink<T, RT, MT>), dim3(s.tiles, s.ksplit, zs), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((expand<T, RT, MT>), dim3(s.tiles, y, z), dim3(256), 0, stream, a);
+  // columns of a workgroup: 256, or more where that still leaves some 1024
+  // workgroups, so that U is added up and split less often
+  const int y = min((a.N + 255) / 256, max(1, 1024 / s.tiles / ze));
+  // R and C beyond the L2s' 32 MiB go past the caches (16384 x 4096, rank 16:
+  // 98 us against 111; 512 rows 16.7 against 15.7)
+  if ((int64_t)a.M * a.N * 4 > ((int64_t)32 << 20))
+    hipLaunchKernelGGL((expand<T, RT, MT, true>), dim3(s.tiles, y, ze), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((expand<T, RT, MT, false>), dim3(s.tiles, y, ze), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename T, int RT>
 hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
-  return s.mt == 2 ? launch<T, RT, 2>(a, s, stream) : launch<T, RT, 1>(a, s, stream);
+  if constexpr (RT <= 4)
+    if (s.mt == 2) return launch<T, RT, 2>(a, s, stream);
+  return launch<T, RT, 1>(a, s, stream);
 }
 
 template <typename T>
@@ -336,14 +492,14 @@ constexpr int64_t kLim = (int64_t)1 << 31;
 // The sizes a call would run (M = 0 included).
 gemm_epi_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters) {
   if (M < 0 || N <= 0 || K <= 0 || rank <= 0 || adapters <= 0) return GEMM_EPI_ERR_INVALID_ARG;
-  if (rank > 128 || rank % 8 != 0 || K % 8 != 0 || M >= kLim / 8 || K > kLim - 256 || adapters > 65535 ||
+  if (rank > 128 || rank % 8 != 0 || K % 8 != 0 || M >= kLim / 8 || K >= kLim / 8 || adapters > 65535 ||
       N > (int64_t)65535 * 256)
     return GEMM_EPI_ERR_UNSUPPORTED;
   return GEMM_EPI_OK;
 }
 
 size_t workspace_bytes(int64_t M, int64_t K, int64_t rank) {
-  return (size_t)cut(M, K).ksplit * (size_t)M * (size_t)rank_pad(rank) * 4;
+  return (size_t)cut(M, K, rank).ksplit * (size_t)M * (size_t)rank_pad(rank) * 4;
 }
 
 }  // namespace lora
@@ -371,7 +527,7 @@ gemm_epi_status gemm_epi_lora(const void* X, int64_t ldx, const void* A, const v
   if (ldx % 8 != 0 || (((uintptr_t)X | (uintptr_t)A | (uintptr_t)B | (uintptr_t)workspace) & 15u))
     return GEMM_EPI_ERR_UNSUPPORTED;
   if (workspace_bytes < ge::lora::workspace_bytes(M, K, rank)) return GEMM_EPI_ERR_INVALID_ARG;
-  const ge::lora::Cut cut = ge::lora::cut(M, K);
+  const ge::lora::Cut cut = ge::lora::cut(M, K, rank);
   const bool vec = (((uintptr_t)C | (uintptr_t)R) & 15u) == 0 && ldc % 8 == 0 && (!R || ldr % 8 == 0);
   const ge::lora::Args a{X,   A,   B,   R,      scale,  ids,       C,           (float*)workspace,
                          ldx, ldr, ldc, (int)M, (int)N, (int)K,    (int)rank,   (int)adapters,

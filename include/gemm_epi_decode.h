@@ -80,8 +80,8 @@ gemm_epi_status gemm_epi_rmsnorm(const void* X, int64_t ldx, const void* R, int6
  * or adapters <= 0, a leading dimension below its row, dtype not F16/BF16,
  * workspace missing or too small, a pointer off its element's alignment),
  * UNSUPPORTED (rank above 128 or not a multiple of 8, K not a multiple of 8,
- * ldx not a multiple of 8, X, A, B or workspace not 16-byte aligned, M >=
- * 2^28, K above 2^31 - 256, N above 65535 * 256, more than 65535 adapters),
+ * ldx not a multiple of 8, X, A, B or workspace not 16-byte aligned, M or K
+ * >= 2^28, N above 65535 * 256, more than 65535 adapters),
  * HIP. */
 gemm_epi_status gemm_epi_lora(const void* X, int64_t ldx, const void* A, const void* B, const float* scale,
                               const int32_t* ids, const void* R, int64_t ldr, void* C, int64_t ldc, int64_t M,

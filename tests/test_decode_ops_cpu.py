@@ -81,12 +81,12 @@ def test_lora_refusals(kw, want):
 def test_lora_workspace_size():
     # a multiple of one fp32 row of the padded rank for each row and range of
     # K; nothing for sizes that are refused
-    for M, K, rank, pad in ((1, 8, 8, 16), (16, 4096, 16, 16), (4096, 4096, 40, 64), (33, 1000, 128, 128)):
-        n = gb.gemm_epi_lora_workspace_size(M, 100, K, rank, 4)
+    size = gb.gemm_epi_lora_workspace_size
+    for M, K, rank, pad in ((1, 8, 8, 16), (16, 4096, 16, 16), (100, 4096, 40, 64), (33, 1000, 128, 128), (20000, 4096, 8, 16)):
+        n = size(M, 100, K, rank, 4)
         assert n > 0 and n % (M * pad * 4) == 0
-    assert gb.gemm_epi_lora_workspace_size(0, 100, 64, 8, 4) == 0
-    assert gb.gemm_epi_lora_workspace_size(4, 100, 64, 12, 4) == 0
-    assert gb.gemm_epi_lora_workspace_size(4, 100, 64, 8, 0) == 0
+    assert size(0, 100, 64, 8, 4) == 0 == size(4, 100, 64, 12, 4) == size(4, 100, 64, 8, 0)
+    assert max(size(M, 100, K, 128, 4) for M in range(1, 2000) for K in (8, 4096, 1 << 20)) < 256 << 20
 
 
 _CACHE = dict(k=P, v=P, k_scale=None, v_scale=None, num_pages=9, page_size=16, heads=2, head_dim=64, dtype="bf16")

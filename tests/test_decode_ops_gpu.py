@@ -221,7 +221,8 @@ def lora_run(x, a, b, ids, s, r, dtype, extra=0, ws=None):
 @pytest.mark.parametrize("M,N,K,rank,adapters", [
     (1, 8, 8, 8, 1), (1, 4096, 4096, 16, 3), (16, 64, 64, 16, 1), (17, 65, 72, 24, 5), (5, 1, 128, 8, 2),
     (33, 1000, 1000, 32, 40), (64, 513, 2048, 64, 16), (100, 255, 520, 128, 7), (31, 96, 8200, 40, 3),
-    (16, 256, 16, 16, 16), (2, 100000, 64, 8, 2), (300, 320, 256, 72, 9)])
+    (16, 256, 16, 16, 16), (2, 100000, 64, 8, 2), (300, 320, 256, 72, 9),
+    (512, 200, 264, 16, 3), (1000, 65, 2056, 24, 5), (777, 1100, 1032, 128, 2), (520, 8, 8, 8, 20), (8200, 72, 136, 40, 6)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_lora(M, N, K, rank, adapters, dtype):
     # ids in no order, some rows without an adapter (-1, and past the last)
@@ -233,8 +234,9 @@ def test_lora(M, N, K, rank, adapters, dtype):
 
 @pytest.mark.parametrize("ids", ["same", "none", "runs", "each"])
 @pytest.mark.parametrize("residual,scale", [(True, False), (False, True)])
-def test_lora_ids(ids, residual, scale):
-    M, adapters = 80, 80
+@pytest.mark.parametrize("M", [80, 600])
+def test_lora_ids(ids, residual, scale, M):
+    adapters = M
     ids = {"same": [3] * M, "none": [-1] * M, "runs": [m // 23 for m in range(M)], "each": list(range(M))}[ids]
     c = lora_case(M, 192, 512, 16, adapters, "bf16", ids, 5, residual=residual, scale=scale)
     lora_check(*c, lora_run(*c, "bf16"), "bf16", "ids")
@@ -248,10 +250,11 @@ def test_lora_out_of_range_ids():
     assert torch.equal(got[3:8].cpu(), c[5][3:8])  # without an adapter: the residual's bits
 
 
-def test_lora_another_adapters_values_stay_out():
+@pytest.mark.parametrize("repeat", [6, 100])
+def test_lora_another_adapters_values_stay_out(repeat):
     # adapter 1 is all NaN and infinities: only its own rows see them
-    ids = [0, 1, 0, 2, -1, 2] * 6
-    x, a, b, i, s, r = lora_case(36, 136, 256, 16, 3, "bf16", ids, 7)
+    ids = [0, 1, 0, 2, -1, 2] * repeat
+    x, a, b, i, s, r = lora_case(6 * repeat, 136, 256, 16, 3, "bf16", ids, 7)
     want = lora_run(x, a, b, i, s, r, "bf16").cpu()
     a[1], b[1] = NAN, float("inf")
     got = lora_run(x, a, b, i, s, r, "bf16").cpu()
@@ -265,15 +268,25 @@ def test_lora_another_adapters_values_stay_out():
     assert torch.equal(got[keep], want[keep]) and bool(got[2].isnan().all())
 
 
+@pytest.mark.parametrize("M", [20, 640])
 @pytest.mark.parametrize("dtype,big", [("f16", 3.0e4), ("bf16", 2.0 ** 90)])
-def test_lora_large_inner_products(dtype, big):
+def test_lora_large_inner_products(dtype, big, M):
     # U far beyond the largest f16, C within it: the two parts of U carry a
     # power of two
-    x, a, b, i, s, r = lora_case(20, 64, 128, 16, 2, dtype, [0, 1] * 10, 8, residual=False)
+    x, a, b, i, s, r = lora_case(M, 64, 128, 16, 2, dtype, [0, 1] * (M // 2), 8, residual=False)
     x = (x.float() * big / 8).to(DT[dtype])
     a = (a.float() * 300).to(DT[dtype])
     b = (b.float() * (2.0 ** -14 if dtype == "f16" else 2.0 ** -90)).to(DT[dtype])
     lora_check(x, a, b, i, s, r, lora_run(x, a, b, i, s, r, dtype), dtype, "large U")
+
+
+def test_lora_many_rows_in_place():
+    x, a, b, i, s, r = c = lora_case(700, 264, 320, 24, 4, "bf16", [(m // 9) % 5 - 1 for m in range(700)], 9)
+    want = lora_run(*c, "bf16")
+    cd = r.cuda()
+    gb.lora(x.cuda(), a.cuda(), b.cuda(), i.cuda(), cd, scale=s.cuda(), residual=cd)
+    torch.cuda.synchronize()
+    assert torch.equal(cd, want)
 
 
 def test_lora_in_place_and_dirty_workspace():
