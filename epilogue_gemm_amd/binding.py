@@ -476,6 +476,8 @@ class PagedCache:
         shape = k.shape
         if len(shape) != 4:
             raise ValueError("k: expected a 4-d tensor [num_pages, heads, page_size, head_dim]")
+        if not k.is_cuda:
+            raise ValueError("k: expected a CUDA tensor")
         fmt = _dtype_name(k)
         if fmt not in ("f16", "bf16", "fp8"):
             raise ValueError(f"k: dtype {k.dtype}; expected float16, bfloat16 or float8_e4m3fn")

@@ -48,25 +48,38 @@ struct AppendArgs {
   int num_pages, page_size, heads, width, batch, tokens;
 };
 
-// 2^e, e the smallest integer >= -100 with amax <= 448 * 2^e; NaN for an
-// infinite or NaN amax.  amax = m 2^k, m in [1/2, 1): 448 = 0.875 * 2^9.
-__device__ __forceinline__ float pow2_scale(float amax) {
-  if (!(amax < __builtin_inff())) return __builtin_nanf("");
-  if (amax == 0.0f) return 0x1p-100f;
+// The smallest integer e >= -100 with amax <= 448 * 2^e, for a finite amax:
+// amax = m 2^k, m in [1/2, 1), and 448 = 0.875 * 2^9.
+__device__ __forceinline__ int scale_exponent(float amax) {
   const int k = __builtin_amdgcn_frexp_expf(amax);
   const int e = k - (__builtin_amdgcn_frexp_mantf(amax) > 0.875f ? 8 : 9);
-  return __builtin_amdgcn_ldexpf(1.0f, max(e, -100));
+  return amax == 0.0f ? -100 : max(e, -100);
 }
 
-// One wave a token: its sequence, page and slot, then the rows of all heads,
-// 8 values a lane.  An E4M3 row's largest value is found over the D / 8
-// lanes that hold it.
+// One wave a token: the first rows' loads, then the token's sequence, page
+// and slot while they are in flight, then the rows of all heads, 8 values a
+// lane.  An E4M3 row's largest value is found over the D / 8 lanes that hold
+// it, by the bits of |x|, which order a NaN above every number.  Bound by
+// memory for many tokens, by the three dependent lookups for few.
 template <typename T, bool FP8, int D>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-  constexpr int LPR = D / 8;  // lanes of a row
+  constexpr int LPR = D / 8;   // lanes of a row
+  constexpr int BATCH = 4;     // pieces of a lane in flight
   const int lane = threadIdx.x & 63;
   const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   if (t >= a.tokens) return;
+  const int n = a.heads * LPR;  // pieces of K, then as many of V
+  const T* k = (const T*)a.K + t * a.ldk;
+  const T* v = (const T*)a.V + t * a.ldv;
+  u32x4 x[BATCH];
+  auto load = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int i = min(i0 + 64 * b, 2 * n - 1);  // (past the last: it again)
+      x[b] = *(const u32x4*)(i >= n ? v + 8 * (i - n) : k + 8 * i);
+    }
+  };
+  load(lane);
   int seq = t, end = t + 1;
   if (a.starts) {
     // the number of sequences whose rows end at or before this one
@@ -83,36 +96,41 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   const int page = page_or_none(a.pages[seq * a.ld + pos / a.page_size], a.num_pages);
   if (page < 0) return;
   const int64_t row0 = row_of(page, a.heads, 0, a.page_size, pos % a.page_size);
-  const int n = a.heads * LPR;
-  for (int i = lane; i < 2 * n; i += 64) {
-    const bool val = i >= n;
-    const int j = val ? i - n : i, head = j / LPR, at = j % LPR;
-    const T* src = val ? (const T*)a.V + t * a.ldv : (const T*)a.K + t * a.ldk;
-    const u32x4 x = *(const u32x4*)(src + 8 * j);
-    const int64_t row = row0 + (int64_t)head * a.page_size;
-    char* dst = val ? a.v : a.k;
-    if constexpr (!FP8) {
-      *(u32x4*)(dst + (row * D + 8 * at) * 2) = x;
-    } else {
-      float f[8];
+  for (int i0 = lane; i0 < 2 * n; i0 += 64 * BATCH) {
+    if (i0 != lane) load(i0);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        f[2 * w] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[w] & 0xffffu)));
-        f[2 * w + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[w] >> 16)));
+    for (int b = 0; b < BATCH; ++b) {
+      const int i = i0 + 64 * b;
+      if (i >= 2 * n) break;
+      const bool val = i >= n;
+      const int j = val ? i - n : i, head = j / LPR, at = j % LPR;
+      const int64_t row = row0 + (int64_t)head * a.page_size;
+      char* dst = val ? a.v : a.k;
+      if constexpr (!FP8) {
+        *(u32x4*)(dst + (row * D + 8 * at) * 2) = x[b];
+      } else {
+        float f[8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          f[2 * w] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[b][w] & 0xffffu)));
+          f[2 * w + 1] = to_f32(__builtin_bit_cast(T, (uint16_t)(x[b][w] >> 16)));
+          mx = max(mx, max(__builtin_bit_cast(uint32_t, f[2 * w]) & 0x7fffffffu,
+                           __builtin_bit_cast(uint32_t, f[2 * w + 1]) & 0x7fffffffu));
+        }
+        // (whole groups of lanes have a row or none)
+        const float amax = __builtin_bit_cast(float, wave::max_over<LPR>(mx));
+        const int e = scale_exponent(amax);
+        const bool number = amax < __builtin_inff();
+        const float inv = number ? __builtin_amdgcn_ldexpf(1.0f, -e) : __builtin_nanf("");
+        // (within +-448, by the scale: no clamp)
+        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
+        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, 0, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+        *(u32x2*)(dst + row * D + 8 * at) = u32x2{(uint32_t)lo, (uint32_t)hi};
+        if (at == 0) (val ? a.vs : a.ks)[row] = number ? __builtin_amdgcn_ldexpf(1.0f, e) : __builtin_nanf("");
       }
-      // by the bits of |x|, which order a NaN above every number
-      uint32_t mx = 0;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) mx = max(mx, __builtin_bit_cast(uint32_t, f[u]) & 0x7fffffffu);
-#pragma unroll
-      for (int m = 1; m < LPR; m <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, m));
-      const float s = pow2_scale(__builtin_bit_cast(float, mx));
-      const float inv = 1.0f / s;
-      u32x2 q;
-      q.x = pack4_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-      q.y = pack4_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-      *(u32x2*)(dst + row * D + 8 * at) = q;
-      if (at == 0) (val ? a.vs : a.ks)[row] = s;
     }
   }
 }

@@ -44,6 +44,17 @@ __device__ __forceinline__ float over_row(float x) {
   return Op::op(x, dpp<0x140>(x));  // row_mirror
 }
 
+// The largest x over the 8 or 16 lanes of a group.
+template <int LANES>
+__device__ __forceinline__ uint32_t max_over(uint32_t x) {
+  static_assert(LANES == 8 || LANES == 16, "half a row or a row");
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true));
+  if constexpr (LANES == 16) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, true));
+  return x;
+}
+
 // x combined over the wave, the same bits in every lane.
 template <typename Op>
 __device__ __forceinline__ float all(float x) {

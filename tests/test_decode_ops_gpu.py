@@ -817,7 +817,7 @@ def test_binding_refusals():
     k8 = k.to(torch.float8_e4m3fn)
     s8 = torch.zeros(3, 2, 16, device="cuda")
     for args in ((k[0], k[0]), (k, k[:2]), (k, k.half()), (k.float(), k.float()), (k, k, s8, s8), (k8, k8), (k8, k8, s8), (k8, k8, s8, s8[:2]),
-                 (k.transpose(1, 2), k)):
+                 (k.transpose(1, 2), k), (k.cpu(), k.cpu())):
         with pytest.raises(ValueError):
             gb.PagedCache(*args)
     cache = gb.PagedCache(k, k.clone())
