@@ -6,12 +6,16 @@
 // row) as fp32 partial sums over ranges of K; `expand` adds the partials in
 // their order, brings U to the input format in two parts and does the second
 // product for a range of columns.  Rows come in any order of adapters: a
-// workgroup takes 16 or 32 consecutive rows -- MFMA operands -- and runs once
+// workgroup takes 16 consecutive rows -- an MFMA operand -- and runs once
 // over each adapter that occurs among them, keeping of each product the rows
-// that are the adapter's; where rows are few, the adapters of a tile are
-// spread over workgroups (grid z).  (Both products in one kernel, U never
-// leaving LDS, was measured slower everywhere: 4096 x 4096 -> 4096, rank 64,
-// 48 us against 38, as a tile's A and B then pass through one CU.)
+// that are the adapter's; where tiles are few, the adapters of a tile are
+// spread over workgroups (grid z).
+//
+// Measured and not kept: both products in one kernel, U never leaving LDS
+// (4096 x 4096 -> 4096, rank 64: 48 us against 41, as all of A and B pass
+// through each CU); tiles of 32 rows (39 against 41 us, but 80 against 56
+// where each row has another adapter) and, for the second product, of 64;
+// B and R one and two turns ahead through a wave's columns (44 us).
 #include "gemm_tile16.hpp"
 #include "wave.hpp"
 
@@ -40,55 +44,44 @@ __device__ __forceinline__ int row_adapter(const Args& a, int row) {
   return id >= 0 && id < a.adapters ? id : -1;
 }
 
-// f(adapter, rows) for each adapter among the 16 MT rows from row0 on, in the
-// order of their first rows, rows a bit mask; uniform over the wave.
-template <int MT, typename F>
-__device__ __forceinline__ void each_adapter(const Args& a, int row0, int lane, F&& f) {
-  const int id = row_adapter(a, row0 + (lane & (16 * MT - 1)));
-  constexpr uint32_t all = MT == 1 ? 0xffffu : 0xffffffffu;
-  uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0) & all;
+// f(adapter, rows) for each adapter among 16 rows, lane l having that of row
+// l % 16, in the order of their first rows, rows a bit mask; uniform over the
+// wave.
+template <typename F>
+__device__ __forceinline__ void each_adapter(int id, F&& f) {
+  uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(id >= 0) & 0xffffu;
   while (todo) {
     const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == ad) & all;
+    const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(id == ad) & 0xffffu;
     todo &= ~rows;
     f(ad, rows);
   }
 }
 
-// Bytes of LDS a wave stages its operands and results in.
-template <int RT, int MT>
-constexpr int wave_bytes() {
-  const int first = (MT + RT) * 2048, second = 64 * (16 * RT + 8) * 2, out = 16 * 68 * 4;
-  return first > second ? (first > out ? first : out) : (second > out ? second : out);
-}
-
-// U^T += A X^T over one of NW waves' part of [kbeg, kend): first operand 16 of
-// the adapter's rows, second 16 rows of X, so that lane (m = l % 16, h = l /
-// 16) receives U[m][16 t + 4 h + e].  A wave's part is contiguous and taken
-// in stages of 64 columns.  Loads take whole cache lines, eight rows of 128
-// bytes an instruction (sixteen half lines, an operand's own shape, cost the
-// L1 twice as long), and change lanes through the wave's own LDS: 16-byte
+// U^T += A X^T over one of four waves' part of [kbeg, kend): first operand 16
+// of the adapter's rows, second the 16 rows of X, so that lane (m = l % 16, h
+// = l / 16) receives U[m][16 t + 4 h + e].  A wave's part is contiguous and
+// taken in stages of 64 columns.  Loads take whole cache lines, eight rows of
+// 128 bytes an instruction (sixteen half lines, an operand's own shape, cost
+// the L1 twice as long), and change lanes through the wave's own LDS: 16-byte
 // chunk x of row r at x ^ (r / 2 % 8), which keeps an operand's 16 rows on
 // different banks.  The next stage's loads are in flight while one is
 // multiplied.  The waves' parts and the tiles' first stages (`turn`) lie
 // apart, for the memory channels' sake.
-template <typename T, int RT, int MT, int NW>
-__device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[MT][RT], int row0, int ad, int kbeg, int kend, char* lds,
+template <typename T, int RT>
+__device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0, int ad, int kbeg, int kend, char* lds,
                                       int wave, int lane, int turn) {
   const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
-  const T* x[MT][2];
+  const T* x[2];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      x[i][j] = (const T*)a.X + (int64_t)min(row0 + 16 * i + 8 * j + lr, a.M - 1) * a.ldx + 8 * lc;
+  for (int j = 0; j < 2; ++j) x[j] = (const T*)a.X + (int64_t)min(row0 + 8 * j + lr, a.M - 1) * a.ldx + 8 * lc;
   const T* ab = (const T*)a.A + (int64_t)ad * a.rank * a.K;
   const uint32_t aoff = (uint32_t)lr * a.K + 8 * lc;
-  const int part = (kend - kbeg + 64 * NW - 1) / (64 * NW) * 64;
+  const int part = (kend - kbeg + 255) / 256 * 64;
   const int k1 = kbeg + part * wave, k2 = min(kend, k1 + part);
   const int stages = k2 > k1 ? (k2 - k1 + 63) / 64 : 0;
   if (stages == 0) return;
-  u32x4 g[MT + RT][2];
+  u32x4 g[1 + RT][2];
   bool in;  // this lane's columns of the stage exist (K is a multiple of 8)
   int at = turn % stages;
   auto load = [&]() __attribute__((always_inline)) {
@@ -98,13 +91,12 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[MT][RT], int r
     const int k = in ? k0 : -8 * lc;  // (else the row's first: a valid address)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) g[i][j] = *(const u32x4*)(x[i][j] + k);
+      g[0][j] = *(const u32x4*)(x[j] + k);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         // eight rows exist or not together, as the rank is a multiple of 8
         const int r = 16 * t + 8 * j < a.rank ? 16 * t + 8 * j : 0;
-        g[MT + t][j] = *(const u32x4*)(ab + (int64_t)r * a.K + (int64_t)k + aoff);
+        g[1 + t][j] = *(const u32x4*)(ab + (int64_t)r * a.K + (int64_t)k + aoff);
       }
     }
   };
@@ -115,11 +107,11 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[MT][RT], int r
   for (int n = 0; n < stages; ++n) {
     if (__builtin_amdgcn_ballot_w64(!in)) {
 #pragma unroll
-      for (int t = 0; t < MT + RT; ++t)
+      for (int t = 0; t < 1 + RT; ++t)
         if (!in) g[t][0] = g[t][1] = u32x4{};
     }
 #pragma unroll
-    for (int t = 0; t < MT + RT; ++t) {
+    for (int t = 0; t < 1 + RT; ++t) {
       *(u32x4*)(w + 2048 * t) = g[t][0];
       *(u32x4*)(w1 + 2048 * t) = g[t][1];
     }
@@ -129,15 +121,9 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[MT][RT], int r
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int chunk = ((4 * s + h) ^ (c >> 1)) << 4;
-      u32x4 xf[MT];
+      const u32x4 xf = *(const u32x4*)(rd + chunk);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) xf[i] = *(const u32x4*)(rd + 2048 * i + chunk);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const u32x4 af = *(const u32x4*)(rd + 2048 * (MT + t) + chunk);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][t] = mfma16<T>(af, xf[i], acc[i][t]);
-      }
+      for (int t = 0; t < RT; ++t) acc[t] = mfma16<T>(*(const u32x4*)(rd + 2048 * (1 + t) + chunk), xf, acc[t]);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -168,196 +154,30 @@ __device__ __forceinline__ int split(const float (&u)[8], u32x4& hi, u32x4& lo) 
   return ex;
 }
 
-// The second product of a wave, C^T = B U^T, for every column n0 + step i, 64
-// columns at a time: first operand 16 rows of B (columns of C), second 16
-// rows of U, so that lane (m, h) receives four columns of row m per product;
-// once for each adapter of list[0 .. count), keeping the rows that are the
-// adapter's.  The 64 rows of B are contiguous and loaded so, then change
-// lanes through the wave's LDS (rows of RP + 8 values, those past the rank
-// zero); C's 16 x 64 change lanes there too, so that R and C move in whole
-// lines, eight rows of 128 bytes an instruction.  The next turn's B and R
-// two turns on are in flight while one is multiplied.  Only the rows of `mine` are written.
-template <typename T, int RT, int MT, bool PAST>
-__device__ __forceinline__ void second(const Args& a, int row0, int n0, int step, const int* list, int count, uint32_t mine,
-                                       const uint16_t (&su)[2][16 * MT][16 * RT + 8], const int* sex, char* lds, int lane) {
-  constexpr int RP = 16 * RT, ST = (RP + 31) / 32, LD = RP + 8, BL = 2 * RT;
-  if (n0 >= a.N) return;
-  const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
-  int id[MT], ex[MT];
-  float back[MT];
-  u32x4 uh[MT][ST], ul[MT][ST];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    id[i] = row_adapter(a, row0 + 16 * i + c);
-    ex[i] = id[i] < 0 ? 0 : sex[16 * i + c];
-    back[i] = id[i] < 0 ? 0.0f : a.scale ? a.scale[id[i]] : 1.0f;
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      const int r = 32 * s + 8 * h;
-      // (rows without an adapter have no U)
-      uh[i][s] = r < RP && id[i] >= 0 ? *(const u32x4*)&su[0][16 * i + c][r] : u32x4{};
-      ul[i][s] = r < RP && id[i] >= 0 ? *(const u32x4*)&su[1][16 * i + c][r] : u32x4{};
-    }
-  }
-  // this lane's 16-byte pieces of 64 rows of B, and where they go in LDS
-  const int pieces = a.rank >> 3;  // of a row; lane + 64 i < 64 pieces for i < pieces
-  int dst[BL];
-#pragma unroll
-  for (int i = 0; i < BL; ++i) {
-    const int q = lane + 64 * i;
-    dst[i] = (q / pieces * LD + q % pieces * 8) * 2;
-  }
-  auto load_b = [&](u32x4(&b)[BL], int ad, int n) __attribute__((always_inline)) {
-    const T* p = (const T*)a.B + ((int64_t)ad * a.N + n) * a.rank;
-    const int most = min(64, a.N - n) * pieces - 1;
-#pragma unroll
-    for (int i = 0; i < BL; ++i)
-      if (i < pieces) b[i] = *(const u32x4*)(p + 8 * min(lane + 64 * i, most));
-  };
-  auto load_r = [&](u32x4(&r)[MT][2], int n) __attribute__((always_inline)) {
-    if (!a.vec || !a.R || n + 64 > a.N) return;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const T* p = (const T*)a.R + (int64_t)min(row0 + 16 * i + 8 * j + lr, a.M - 1) * a.ldr + n + 8 * lc;
-        r[i][j] = PAST ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p;
-      }
-  };
-  // C for the 64 columns from n on
-  auto store = [&](const f32x4(&out)[MT][4], const u32x4(&r)[MT][2], int n) __attribute__((always_inline)) {
-    const bool vec = a.vec && n + 64 <= a.N;
-    float* const f = (float*)lds;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = id[i] < 0 ? 0.0f : __builtin_amdgcn_ldexpf(out[i][j][e], ex[i]) * back[i];
-        *(f32x4*)(f + c * 68 + 16 * j + 4 * h) = v;
-      }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int m = 16 * i + 8 * j + lr, row = row0 + m, at = n + 8 * lc;
-        const f32x4 v0 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc), v1 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc + 4);
-        float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-        if (row >= a.M || !(mine >> m & 1)) continue;
-        T* cp = (T*)a.C + (int64_t)row * a.ldc + at;
-        if (vec) {
-          if (a.R) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[2 * e] += to_f32(__builtin_bit_cast(T, (uint16_t)(r[i][j][e] & 0xffffu)));
-              v[2 * e + 1] += to_f32(__builtin_bit_cast(T, (uint16_t)(r[i][j][e] >> 16)));
-            }
-          }
-          u32x4 w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack2_out<T>(v[2 * e], v[2 * e + 1]);
-          if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4*)cp);
-          else *(u32x4*)cp = w;
-        } else {
-          const T* rp = a.R ? (const T*)a.R + (int64_t)row * a.ldr + at : nullptr;
-          for (int e = 0; e < 8; ++e)
-            if (at + e < a.N) cp[e] = from_f32<T>(v[e] + (rp ? to_f32(rp[e]) : 0.0f));
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
-  };
-  f32x4 out[MT][4] = {};
-  u32x4 r0[MT][2], r1[MT][2], r2[MT][2];
-  if (count == 0) {  // no adapter: C = R
-    for (; n0 < a.N; n0 += step) {
-      load_r(r0, n0);
-      store(out, r0, n0);
-    }
-    return;
-  }
-  // the turns: each adapter for 64 columns, then the next 64
-  u32x4 b[BL];
-  int k = 0;
-  load_b(b, __builtin_amdgcn_readfirstlane(list[0]), n0);
-  load_r(r0, n0);
-  load_r(r1, n0 + step < a.N ? n0 + step : n0);
-  const char* const rd = lds + 16 * h;
-  for (;;) {
-    const int ad = __builtin_amdgcn_readfirstlane(list[k]);
-    // B to LDS; columns past the rank are zero
-#pragma unroll
-    for (int i = 0; i < BL; ++i)
-      if (i < pieces) *(u32x4*)(lds + dst[i]) = b[i];
-    if (a.rank < 32 * ST)
-      for (int i = a.rank; i < 32 * ST && i < LD; i += 8) *(u32x4*)(lds + (lane * LD + i) * 2) = u32x4{};
-    __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses are done in order)
-    // the next turn's loads (past the last: this one's again)
-    const int kn = k + 1 == count ? 0 : k + 1, nn = kn == 0 ? n0 + step : n0;
-    const bool more = nn < a.N;
-    load_b(b, __builtin_amdgcn_readfirstlane(list[kn]), more ? nn : n0);
-    if (kn == 0) load_r(r2, nn + step < a.N ? nn + step : n0);
-    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the products
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 bf[ST];
-#pragma unroll
-      for (int s = 0; s < ST; ++s)
-        bf[s] = 32 * s + 8 * h < LD ? *(const u32x4*)(rd + ((16 * j + c) * LD + 32 * s) * 2) : u32x4{};
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        f32x4 acc = {};
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-          acc = mfma16<T>(bf[s], uh[i][s], acc);
-          acc = mfma16<T>(bf[s], ul[i][s], acc);
-        }
-        if (id[i] == ad) out[i][j] = acc;
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (kn == 0) {
-      store(out, r0, n0);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        r0[i][0] = r1[i][0];
-        r0[i][1] = r1[i][1];
-        r1[i][0] = r2[i][0];
-        r1[i][1] = r2[i][1];
-      }
-    }
-    if (!more) return;
-    n0 = nn;
-    k = kn;
-  }
-}
-
 // U's partial sums.  Workgroup (tile, range, z) takes the adapters number z, z
-// + Z, ... of its 16 MT rows; its four waves add up in LDS.
-template <typename T, int RT, int MT>
+// + Z, ... of its 16 rows; its four waves add up in LDS.
+template <typename T, int RT>
 __global__ __launch_bounds__(256) void shrink(Args a) {
-  constexpr int RP = 16 * RT, ROWS = 16 * MT, PER = wave_bytes<RT, MT>();
-  static_assert(ROWS * (RP + 1) * 4 <= PER, "a wave's sums take the place of its operands");
+  constexpr int RP = 16 * RT, PER = (1 + RT) * 2048;
+  static_assert(16 * (RP + 1) * 4 <= PER, "a wave's sums take the place of its operands");
   __shared__ __attribute__((aligned(16))) char lds[4 * PER];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, h = lane >> 4;
-  const int row0 = blockIdx.x * ROWS;
+  const int row0 = blockIdx.x * 16;
   const int kbeg = blockIdx.y * a.kper, kend = min(a.K, kbeg + a.kper);
   uint32_t number = 0;
-  each_adapter<MT>(a, row0, lane, [&](int ad, uint32_t rows) {
+  each_adapter(row_adapter(a, row0 + c), [&](int ad, uint32_t rows) {
     if (number++ % gridDim.z != blockIdx.z) return;
-    f32x4 acc[MT][RT] = {};
-    inner<T, RT, MT, 4>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
+    f32x4 acc[RT] = {};
+    inner<T, RT>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
     __syncthreads();  // every wave has read its operands: their place holds the sums
     float* red = (float*)(lds + wave * PER);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[(16 * i + c) * (RP + 1) + 16 * t + 4 * h + e] = acc[i][t][e];
+      for (int e = 0; e < 4; ++e) red[c * (RP + 1) + 16 * t + 4 * h + e] = acc[t][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < ROWS * RP; i += 256) {
+    for (int i = threadIdx.x; i < 16 * RP; i += 256) {
       const int m = i / RP, r = i % RP;
       float sum = 0.0f;
 #pragma unroll
@@ -368,43 +188,75 @@ __global__ __launch_bounds__(256) void shrink(Args a) {
   });
 }
 
-// The second product.  The workgroup adds up its rows' partials, eight values
-// a thread, leaves U's two parts in LDS, and each wave takes every fourth 64
-// columns of the workgroup's.  PAST: R and C are more than the caches hold and
-// move past them.
-template <typename T, int RT, int MT, bool PAST>
+// The second product, C^T = B U^T: first operand 16 rows of B (columns of C),
+// second the 16 rows of U, so that lane (m, h) receives four columns of row m
+// per product.  A workgroup has 16 rows and 256 columns at a time, 64 a wave;
+// it adds up its rows' partials of U, eight values a thread, and leaves U's
+// two parts in LDS.  The 64 rows of B of a wave are contiguous and loaded so,
+// then change lanes through the wave's LDS; C changes lanes there too, so
+// that R and C move in whole lines, eight rows of 128 bytes an instruction.
+// The loads of the first columns are all issued before the first wait.
+// Workgroup (tile, columns, z) takes the adapters number z, z + Z, ... of its
+// rows, the first also the rows without one.  PAST: R and C are more than the
+// caches hold and move past them.  Bound by R and C, and for small problems
+// by the chain of ids, U and the LDS's two turns.
+template <typename T, int RT, bool PAST>
 __global__ __launch_bounds__(256) void expand(Args a) {
-  constexpr int RP = 16 * RT, ROWS = 16 * MT, PIECES = RP / 8, PER = wave_bytes<RT, MT>();
+  constexpr int RP = 16 * RT, ST = (RP + 31) / 32, LD = RP + 8;
+  constexpr int PIECES = RP / 8, BL = 2 * RT;  // of a row of U; of a lane in 64 rows of B
+  constexpr int PER = 64 * LD * 2 > 16 * 68 * 4 ? 64 * LD * 2 : 16 * 68 * 4;
   __shared__ __attribute__((aligned(16))) char lds[4 * PER];
-  __shared__ __attribute__((aligned(16))) uint16_t su[2][ROWS][RP + 8];
-  __shared__ int sex[ROWS], list[ROWS];
+  __shared__ __attribute__((aligned(16))) uint16_t su[2][16][LD];
+  __shared__ int sex[16], list[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row0 = blockIdx.x * ROWS;
-  // the rows of the adapters that are this workgroup's; those without one are
-  // the first workgroup's
-  uint32_t mine = 0;
-  int count = 0;
+  const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
+  const int row0 = blockIdx.x * 16;
+  const int id = row_adapter(a, row0 + c);
+  uint32_t mine = 0;  // the rows this workgroup writes
+  int count = 0, first = 0;
   {
     uint32_t number = 0, some = 0;
-    each_adapter<MT>(a, row0, lane, [&](int ad, uint32_t rows) {
+    each_adapter(id, [&](int ad, uint32_t rows) {
       some |= rows;
       if (number++ % gridDim.z == blockIdx.z) {
         mine |= rows;
         if (threadIdx.x == 0) list[count] = ad;
-        ++count;
+        if (count++ == 0) first = ad;
       }
     });
     if (mine == 0 && blockIdx.z != 0) return;
-    if (blockIdx.z == 0) mine |= ~some;
+    if (blockIdx.z == 0) mine |= ~some & 0xffffu;
   }
+  if (mine == 0) return;  // (every row is another workgroup's)
+  char* const wl = lds + wave * PER;
+  const int pieces = a.rank >> 3;  // of a row of B
+  u32x4 b[BL], r[2];
+  auto load_b = [&](int ad, int n) __attribute__((always_inline)) {
+    const T* p = (const T*)a.B + ((int64_t)ad * a.N + n) * a.rank;
+    const int most = min(64, a.N - n) * pieces - 1;
 #pragma unroll
-  for (int i0 = 0; i0 < ROWS * PIECES; i0 += 256) {
-    const int i = i0 + threadIdx.x, m = i / PIECES, r = i % PIECES * 8;
-    if (ROWS * PIECES % 256 != 0 && i >= ROWS * PIECES) break;
-    const int row = row0 + m;
+    for (int i = 0; i < BL; ++i) b[i] = *(const u32x4*)(p + 8 * min(lane + 64 * i, most));
+  };
+  // R's rows 8 j + lr; for a row that is not ours, one that is
+  auto load_r = [&](int n) __attribute__((always_inline)) {
+    if (!a.R || !a.vec || n + 64 > a.N) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int m = mine >> (8 * j + lr) & 1 ? 8 * j + lr : __builtin_ctz(mine);
+      const T* p = (const T*)a.R + (int64_t)min(row0 + m, a.M - 1) * a.ldr + n + 8 * lc;
+      r[j] = PAST ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p;
+    }
+  };
+  const int step = gridDim.y * 256;
+  int n0 = (blockIdx.y * 4 + wave) * 64;
+  load_b(first, min(n0, a.N - 1));  // (no adapter: the first one's, not used)
+  load_r(n0);
+  const float back = id >= 0 && a.scale ? a.scale[id] : 1.0f;
+  if (threadIdx.x < 16 * PIECES) {
+    const int m = threadIdx.x / PIECES, x = threadIdx.x % PIECES * 8;
     float u[8] = {};
-    if (r < a.rank && row < a.M && (mine >> m & 1)) {
-      const float* up = a.U + (int64_t)row * RP + r;
+    if (x < a.rank && row0 + m < a.M && (mine >> m & 1)) {
+      const float* up = a.U + (int64_t)(row0 + m) * RP + x;
 #pragma unroll 8
       for (int p = 0; p < a.ksplit; ++p) {
         const f32x4 lo = *(const f32x4*)(up + (int64_t)p * a.M * RP), hi = *(const f32x4*)(up + (int64_t)p * a.M * RP + 4);
@@ -417,29 +269,106 @@ __global__ __launch_bounds__(256) void expand(Args a) {
     }
     u32x4 hi, lo;
     const int ex = split<T, PIECES>(u, hi, lo);
-    *(u32x4*)&su[0][m][r] = hi;
-    *(u32x4*)&su[1][m][r] = lo;
-    if (r == 0) sex[m] = ex;
+    *(u32x4*)&su[0][m][x] = hi;
+    *(u32x4*)&su[1][m][x] = lo;
+    if (x == 0) sex[m] = ex;
   }
   __syncthreads();
-  second<T, RT, MT, PAST>(a, row0, (blockIdx.y * 4 + wave) * 64, gridDim.y * 256, list, count, mine, su, sex, lds + wave * PER, lane);
+  const int ex = sex[c];
+  u32x4 uh[ST], ul[ST];
+#pragma unroll
+  for (int s = 0; s < ST; ++s) {
+    const int x = 32 * s + 8 * h;
+    uh[s] = x < RP ? *(const u32x4*)&su[0][c][x] : u32x4{};
+    ul[s] = x < RP ? *(const u32x4*)&su[1][c][x] : u32x4{};
+  }
+  for (; n0 < a.N; n0 += step) {
+    f32x4 out[4] = {};
+    for (int k = 0; k < count; ++k) {
+      const int ad = __builtin_amdgcn_readfirstlane(list[k]);
+      if (k > 0) load_b(ad, n0);
+#pragma unroll
+      for (int i = 0; i < BL; ++i)
+        if (i < pieces) {
+          const int q = lane + 64 * i, m = q / pieces;
+          *(u32x4*)(wl + (m * LD + (q - m * pieces) * 8) * 2) = b[i];
+        }
+      __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses are done in order)
+      u32x4 bf[4][ST];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < ST; ++s) bf[j][s] = *(const u32x4*)(wl + ((16 * j + c) * LD + min(32 * s + 8 * h, RP)) * 2);
+      if (a.rank < 32 * ST) {  // past the rank: whatever stands there counts as zero
+#pragma unroll
+        for (int s = 0; s < ST; ++s)
+          if (32 * s + 8 * h >= a.rank) bf[0][s] = bf[1][s] = bf[2][s] = bf[3][s] = u32x4{};
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f32x4 acc = {};
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+          acc = mfma16<T>(bf[j][s], uh[s], acc);
+          acc = mfma16<T>(bf[j][s], ul[s], acc);
+        }
+        if (id == ad) out[j] = acc;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    // C = R + 2^ex back out; the 16 x 64 change lanes: rows 8 j + lr
+    float* const f = (float*)wl;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = id < 0 ? 0.0f : __builtin_amdgcn_ldexpf(out[j][e], ex) * back;
+      *(f32x4*)(f + c * 68 + 16 * j + 4 * h) = x;
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const f32x4 v0 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc), v1 = *(const f32x4*)(f + (8 * j + lr) * 68 + 8 * lc + 4);
+      float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+      const int row = row0 + 8 * j + lr, n = n0 + 8 * lc;
+      if (row >= a.M || !(mine >> (8 * j + lr) & 1)) continue;
+      T* cp = (T*)a.C + (int64_t)row * a.ldc + n;
+      if (a.vec && n0 + 64 <= a.N) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = a.R ? r[j][e] : 0u;
+          w[e] = pack2_out<T>(v[2 * e] + to_f32(__builtin_bit_cast(T, (uint16_t)(x & 0xffffu))),
+                              v[2 * e + 1] + to_f32(__builtin_bit_cast(T, (uint16_t)(x >> 16))));
+        }
+        if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4*)cp);
+        else *(u32x4*)cp = w;
+      } else {
+        const T* rp = a.R ? (const T*)a.R + (int64_t)row * a.ldr + n : nullptr;
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N) cp[e] = from_f32<T>(v[e] + (rp ? to_f32(rp[e]) : 0.0f));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (n0 + step < a.N) {
+      load_b(first, n0 + step);
+      load_r(n0 + step);
+    }
+  }
 }
 
-// How a problem is cut, by its sizes alone.
+// Ranges of K, by the sizes alone.  Up to 1024 rows eight of 512 or more,
+// which give the chip work (K = N = 4096: 16 rows 8.7 us, one range 11.1; 512
+// rows, rank 64, 15.3 against 20.2); more rows one, as partial sums then cost
+// what the ranges gain (4096 rows, rank 64: 43.4 us, two 44.8, four 42.6; rank
+// 16 29.0, 29.0, 30.4).
 struct Cut {
-  int mt, tiles;     // tiles of 16 mt rows
-  int ksplit, kper;  // ranges of K
+  int tiles, ksplit, kper;
 };
-inline Cut cut(int64_t M, int64_t K, int64_t rank) {
+inline Cut cut(int64_t M, int64_t K) {
+  const int64_t ks = M > 1024 ? 1 : K >= 4096 ? 8 : (K + 511) / 512;
   Cut s;
-  // 32 rows share an adapter's values where there are tiles enough (16384
-  // rows, rank 64: 122 us against 139)
-  s.mt = M >= 8192 && rank <= 64 ? 2 : 1;
-  s.tiles = (int)((M + 16 * s.mt - 1) / (16 * s.mt));
-  // ranges of K: some 256 workgroups, one stage of their waves or more each
-  int64_t ks = s.tiles >= 256 ? 1 : 256 / s.tiles;
-  const int64_t most = (K + 255) / 256;
-  if (ks > most) ks = most;
+  s.tiles = (int)((M + 15) / 16);
   s.kper = (int)(((K + ks - 1) / ks + 255) / 256 * 256);
   s.ksplit = (int)((K + s.kper - 1) / s.kper);
   return s;
@@ -450,31 +379,23 @@ inline int64_t rank_pad(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32
 // Workgroups among which a tile's adapters are spread (grid z): as many as it
 // can hold where tiles are few.  Those that find no adapter of theirs end at
 // once; `expand`, whose rows cost more than its adapters, spreads less.
-template <typename T, int RT, int MT>
+template <typename T, int RT>
 hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
   const int most = min(a.adapters, min(a.M, 16));
-  const int zs = s.tiles <= 4 ? most : s.tiles <= 256 ? min(most, 4) : 1;
-  const int ze = s.tiles <= 4 ? most : s.tiles <= 32 ? min(most, 4) : 1;
-  hipLaunchKernelGGL((shrink<T, RT, MT>), dim3(s.tiles, s.ksplit, zs), dim3(256), 0, stream, a);
+  const int z1 = s.tiles <= 4 ? most : s.tiles <= 256 ? min(most, 4) : 1;
+  const int z2 = s.tiles <= 4 ? most : s.tiles <= 32 ? min(most, 4) : 1;
+  hipLaunchKernelGGL((shrink<T, RT>), dim3(s.tiles, s.ksplit, z1), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // columns of a workgroup: 256, or more where that still leaves some 1024
-  // workgroups, so that U is added up and split less often
-  const int y = min((a.N + 255) / 256, max(1, 1024 / s.tiles / ze));
-  // R and C beyond the L2s' 32 MiB go past the caches (16384 x 4096, rank 16:
-  // 98 us against 111; 512 rows 16.7 against 15.7)
+  // workgroups; R and C beyond the L2s' 32 MiB go past the caches (16384 x
+  // 4096, rank 16: 98 us against 111; 512 rows 16.7 against 15.7)
+  const int y = min((a.N + 255) / 256, max(1, 1024 / s.tiles / z2));
   if ((int64_t)a.M * a.N * 4 > ((int64_t)32 << 20))
-    hipLaunchKernelGGL((expand<T, RT, MT, true>), dim3(s.tiles, y, ze), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((expand<T, RT, true>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((expand<T, RT, MT, false>), dim3(s.tiles, y, ze), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((expand<T, RT, false>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
   return hipGetLastError();
-}
-
-template <typename T, int RT>
-hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
-  if constexpr (RT <= 4)
-    if (s.mt == 2) return launch<T, RT, 2>(a, s, stream);
-  return launch<T, RT, 1>(a, s, stream);
 }
 
 template <typename T>
@@ -499,7 +420,7 @@ gemm_epi_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t rank, int64
 }
 
 size_t workspace_bytes(int64_t M, int64_t K, int64_t rank) {
-  return (size_t)cut(M, K, rank).ksplit * (size_t)M * (size_t)rank_pad(rank) * 4;
+  return (size_t)cut(M, K).ksplit * (size_t)M * (size_t)rank_pad(rank) * 4;
 }
 
 }  // namespace lora
@@ -527,7 +448,7 @@ gemm_epi_status gemm_epi_lora(const void* X, int64_t ldx, const void* A, const v
   if (ldx % 8 != 0 || (((uintptr_t)X | (uintptr_t)A | (uintptr_t)B | (uintptr_t)workspace) & 15u))
     return GEMM_EPI_ERR_UNSUPPORTED;
   if (workspace_bytes < ge::lora::workspace_bytes(M, K, rank)) return GEMM_EPI_ERR_INVALID_ARG;
-  const ge::lora::Cut cut = ge::lora::cut(M, K, rank);
+  const ge::lora::Cut cut = ge::lora::cut(M, K);
   const bool vec = (((uintptr_t)C | (uintptr_t)R) & 15u) == 0 && ldc % 8 == 0 && (!R || ldr % 8 == 0);
   const ge::lora::Args a{X,   A,   B,   R,      scale,  ids,       C,           (float*)workspace,
                          ldx, ldr, ldc, (int)M, (int)N, (int)K,    (int)rank,   (int)adapters,
