@@ -347,33 +347,41 @@ def _packed(name, t, dtype, shape, index):
     return t.data_ptr()
 
 
-def _half_format(name, t):
-    """Format code of a 16-bit tensor."""
-    n = _dtype_name(t)
-    if n != "bf16" and n != "f16":
-        raise ValueError(f"{name}: dtype {t.dtype}; expected float16 or bfloat16")
-    return DTYPES[n]
+class _Torch:
+    """What the calls below use of torch, looked up at the first one."""
+    half = None  # torch.dtype -> format code of the 16-bit formats
 
 
-def _device_and_stream(torch, stream):
-    """(current device, hipStream_t of `stream` or of torch's current stream)."""
-    if stream is None:
-        get, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if get is not None and raw is not None and torch.cuda.is_initialized():
-            index = get()
-            return index, raw(index)
-        return torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
-    index = torch.cuda.current_device()
+def _torch():
+    import torch
+
+    T = _Torch
+    T.torch, T.i32, T.f32, T.fp8 = torch, torch.int32, torch.float32, torch.float8_e4m3fn
+    T.device, T.raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if T.device is None or T.raw is None:
+        T.device, T.raw = torch.cuda.current_device, lambda index: torch.cuda.current_stream(index).cuda_stream
+    torch.cuda.current_device()  # (initialises the device)
+    load_library()
+    T.half = {torch.float16: DTYPES["f16"], torch.bfloat16: DTYPES["bf16"]}
+
+
+def _stream_of(stream, index):
+    """hipStream_t of a given stream, which has to be the current device's."""
     if stream.device.index != index:
         raise ValueError(f"stream: on device {stream.device.index}, the current device is {index}")
-    return index, stream.cuda_stream
+    return stream.cuda_stream
 
 
-def _workspace(torch, workspace, need, index, stream, zeros=0):
+def _not_half(name, t):
+    raise ValueError(f"{name}: dtype {t.dtype}; expected float16 or bfloat16")
+
+
+def _workspace(workspace, need, index, stream, zeros=0):
     """(pointer, bytes) of the caller's workspace, or of one of `need()` bytes,
     the first `zeros` of them zero, from torch's allocator on the stream of
     the call."""
     if workspace is None:
+        torch = _Torch.torch
         with torch.cuda.stream(stream):  # (None: the current one)
             workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
             if zeros:
@@ -390,13 +398,14 @@ def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e
     itself.  ``y`` is of the same format, or float8_e4m3fn with
     ``y_scale`` ([rows] float32) receiving each row's scale.  Enqueued on
     torch's current stream (or `stream`), not synchronised."""
-    import torch
-
-    index, s = _device_and_stream(torch, stream)
+    T = _Torch
+    if T.half is None:
+        _torch()
+    index = T.device()
     shape, dt = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError("x: expected a 2-d tensor [rows, cols]")
-    fmt = out = _half_format("x", x)
+    fmt = out = T.half[dt] if dt in T.half else _not_half("x", x)
     rows, cols = shape
     ldx, w = _rows2("x", x, dt, shape, index), _packed("weight", weight, dt, (cols,), index)
     r = h = sc = None
@@ -406,13 +415,13 @@ def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e
     if residual_out is not None:
         ldh, h = _rows2("residual_out", residual_out, dt, shape, index), residual_out.data_ptr()
     if y_scale is not None:
-        out, dt = DTYPES["fp8"], torch.float8_e4m3fn
-        sc = _packed("y_scale", y_scale, torch.float32, (rows,), index)
+        out, dt = 3, T.fp8  # DTYPES["fp8"]
+        sc = _packed("y_scale", y_scale, T.f32, (rows,), index)
     ldy = _rows2("y", y, dt, shape, index)
     if rows == 0:
         return
-    st = (_lib or load_library()).gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, sc, rows,
-                                                   cols, eps, fmt, out, s)
+    st = _lib.gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, sc, rows, cols, eps, fmt, out,
+                               T.raw(index) if stream is None else _stream_of(stream, index))
     if st != OK:
         raise GemmEpiError("gemm_epi_rmsnorm", st)
 
@@ -431,30 +440,30 @@ def lora(x, a, b, ids, c, scale=None, residual=None, workspace=None, stream=None
     ``workspace``: an optional CUDA tensor of ``lora_workspace_size`` bytes,
     else one is allocated.  With residual None, c is what ``Plan.run`` of the
     projection takes as its residual."""
-    import torch
-
-    index, s = _device_and_stream(torch, stream)
+    T = _Torch
+    if T.half is None:
+        _torch()
+    index = T.device()
     xs, sa, sb, dt = x.shape, a.shape, b.shape, x.dtype
     if len(xs) != 2 or len(sa) != 3 or len(sb) != 3:
         raise ValueError("x, a, b: expected tensors [M, K], [adapters, rank, K] and [adapters, N, rank]")
-    fmt = _half_format("x", x)
-    (M, K), (adapters, rank), N = xs, sa[:2], sb[1]
+    fmt = T.half[dt] if dt in T.half else _not_half("x", x)
+    (M, K), (adapters, rank, _), N = xs, sa, sb[1]
     cs = (M, N)
     ldx = _rows2("x", x, dt, xs, index)
     pa, pb = _packed("a", a, dt, (adapters, rank, K), index), _packed("b", b, dt, (adapters, N, rank), index)
-    pi = _packed("ids", ids, torch.int32, (M,), index)
+    pi = _packed("ids", ids, T.i32, (M,), index)
     ldc = _rows2("c", c, dt, cs, index)
-    ps = None if scale is None else _packed("scale", scale, torch.float32, (adapters,), index)
+    ps = None if scale is None else _packed("scale", scale, T.f32, (adapters,), index)
     pr, ldr = None, 0
     if residual is not None:
         ldr, pr = _rows2("residual", residual, dt, cs, index), residual.data_ptr()
     if M == 0:
         return
-    lib = _lib or load_library()
-    ws, nbytes = _workspace(torch, workspace, lambda: lib.gemm_epi_lora_workspace_size(M, N, K, rank, adapters), index,
-                            stream)
-    st = lib.gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
-                           ws, nbytes, s)
+    s = T.raw(index) if stream is None else _stream_of(stream, index)
+    ws, nbytes = _workspace(workspace, lambda: lora_workspace_size(M, N, K, rank, adapters), index, stream)
+    st = _lib.gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
+                            ws, nbytes, s)
     if st != OK:
         raise GemmEpiError("gemm_epi_lora", st)
 
@@ -494,14 +503,14 @@ class PagedCache:
         self.num_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = paged_cache_struct(pk, pv, pks, pvs, shape[0], shape[2], shape[1], shape[3], fmt)
 
-    def _table(self, torch, pages, lens, index):
+    def _table(self, pages, lens, index):
         if index != self.device_index:
             raise ValueError(f"the cache is on device {self.device_index}, the current device is {index}")
         shape = pages.shape
         if len(shape) != 2:
             raise ValueError("pages: expected a 2-d tensor [batch, width]")
         batch, width = shape
-        i32 = torch.int32
+        i32 = _Torch.i32
         return _PageTable(pages.data_ptr(), _rows2("pages", pages, i32, shape, index), width,
                           _packed("lens", lens, i32, (batch,), index), batch), batch
 
@@ -510,17 +519,19 @@ class PagedCache:
         strided) to their sequences' last positions.  ``starts`` [batch + 1]
         int32: the rows of sequence i are starts[i] .. starts[i + 1] - 1, rows
         from starts[batch] on are ignored; None: one row a sequence."""
-        import torch
-
-        index, s = _device_and_stream(torch, stream)
-        table, batch = self._table(torch, pages, lens, index)
-        fmt, dt = _half_format("k", k), k.dtype
+        T = _Torch
+        if T.half is None:
+            _torch()
+        index = T.device()
+        table, batch = self._table(pages, lens, index)
+        dt = k.dtype
+        fmt = T.half[dt] if dt in T.half else _not_half("k", k)
         tokens = k.shape[0]
         shape = (tokens, self.heads, self.head_dim)
         ldk, ldv = _rows3("k", k, dt, shape, index), _rows3("v", v, dt, shape, index)
-        p = None if starts is None else _packed("starts", starts, torch.int32, (batch + 1,), index)
-        st = (_lib or load_library()).gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                                            p, tokens, fmt, s)
+        p = None if starts is None else _packed("starts", starts, T.i32, (batch + 1,), index)
+        st = _lib.gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv, p, tokens, fmt,
+                                        T.raw(index) if stream is None else _stream_of(stream, index))
         if st != OK:
             raise GemmEpiError("gemm_epi_cache_append", st)
 
@@ -536,11 +547,13 @@ class PagedCache:
         ``workspace_size`` bytes, its first ATTENTION_DECODE_COUNTER_BYTES
         zero before its first use (every completed run leaves them zero), else
         one is allocated."""
-        import torch
-
-        index, s = _device_and_stream(torch, stream)
-        table, batch = self._table(torch, pages, lens, index)
-        fmt, dt = _half_format("q", q), q.dtype
+        T = _Torch
+        if T.half is None:
+            _torch()
+        index = T.device()
+        table, batch = self._table(pages, lens, index)
+        dt = q.dtype
+        fmt = T.half[dt] if dt in T.half else _not_half("q", q)
         shape = q.shape
         if len(shape) != 3:
             raise ValueError("q: expected a 3-d tensor [batch, q_heads, head_dim]")
@@ -549,10 +562,11 @@ class PagedCache:
         ldq, ldo = _rows3("q", q, dt, shape, index), _rows3("o", o, dt, shape, index)
         if batch == 0:
             return
-        ws, nbytes = _workspace(torch, workspace, lambda: self.workspace_size(heads, pages), index, stream,
+        s = T.raw(index) if stream is None else _stream_of(stream, index)
+        ws, nbytes = _workspace(workspace, lambda: self.workspace_size(heads, pages), index, stream,
                                 ATTENTION_DECODE_COUNTER_BYTES)
-        st = (_lib or load_library()).gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(),
-                                                                ldo, heads, fmt, ws, nbytes, s)
+        st = _lib.gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(), ldo, heads, fmt, ws,
+                                            nbytes, s)
         if st != OK:
             raise GemmEpiError("gemm_epi_attention_decode", st)
 
