@@ -299,6 +299,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   using Tl = Tile<FP8, D>;
   constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW, RB = Tl::RB;
   constexpr int KS = D / 32;  // 32-deep steps of a score
+  // 8-bit rows of f16 values up to 65504 have codes times scales up to 65536,
+  // which f16 does not hold: both products take f16's values halved
+  constexpr float kHalf = FP8 && __is_same(T, f16) ? 0.5f : 1.0f;
   __shared__ float sm[4][16], sl[4][16];
   __shared__ __attribute__((aligned(16))) float so[4][16][D + 4];
   __shared__ int last_arrived;
@@ -435,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
           const u32x4 x = kf[i];
-          const float f = t.ks[g];
+          const float f = t.ks[g] * kHalf;
           const u32x4 lo = {widen2<T, false>(x[0], f), widen2<T, true>(x[0], f), widen2<T, false>(x[1], f),
                             widen2<T, true>(x[1], f)};
           const u32x4 hi = {widen2<T, false>(x[2], f), widen2<T, true>(x[2], f), widen2<T, false>(x[3], f),
@@ -447,7 +450,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(kf[i], qf[i], s[g]);
       }
-      s[g] *= a.scale_log2;
+      s[g] *= a.scale_log2 * (1.0f / kHalf);
     }
     if (!whole) {
 #pragma unroll
@@ -486,7 +489,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if constexpr (FP8) {
-        const float f = t.vs[u >> 2][u & 3];
+        const float f = t.vs[u >> 2][u & 3] * kHalf;
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           vr[u][2 * w] = widen2<T, false>(t.v[u][w], f);
@@ -562,6 +565,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) o[j] += x * so[i][qh][d0 + j];
     }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) o[j] *= 1.0f / kHalf;
     if (take == units) {
       const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
       T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
@@ -637,7 +642,6 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
   if (pieces == 1 || joined_here(pieces, min(16, a.group - qg / 16 * 16), D)) return;
   join_rows<T, D>(a, w0, pieces, qg % 16, 1, (T*)a.O + seq * a.ldo + (int64_t)qhead * D, lds);
 }
-
 
 template <typename T, bool FP8, int D>
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream) {

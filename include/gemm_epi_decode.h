@@ -173,14 +173,16 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
  *   Q   [batch, q_heads, head_dim], ldq elements between sequences, format
  *       `dtype` (F16 or BF16), that of the cache unless that is FP8_E4M3
  *   O   [batch, q_heads, head_dim], ldo elements between sequences, `dtype`
- * q_heads is a multiple of the cache's heads.  What the cache holds at or
- * past a sequence's length, in pages of no sequence or in the scales there
- * is read into no result, NaN included.
+ * O overlaps nothing else.  q_heads is a multiple of the cache's heads.  What
+ * the cache holds at or past a sequence's length, in pages of no sequence or
+ * in the scales there is read into no result, NaN included.
  * Scores, softmax and accumulation in fp32; the probabilities enter the
  * second product as two 16-bit parts (their rounded value and its rounded
- * remainder); O is rounded once.  The keys are split over workgroups by the
- * lengths found on the device and joined in a fixed order: the same inputs
- * give the same bits.
+ * remainder); an FP8_E4M3 cache's values enter the products in the format of
+ * Q: exactly, but in F16 those below 2^-13 to a multiple of 2^-23 and those
+ * of a scale above 2^8 perhaps as infinities; O is rounded once.  The keys
+ * are split over workgroups by the lengths found on the device and joined in
+ * a fixed order: the same inputs give the same bits.
  * workspace: gemm_epi_attention_decode_workspace_size bytes, 16-byte aligned.
  * Its first GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES hold counters: zero-filled
  * once before its first use, and left zero by every run that completes; the

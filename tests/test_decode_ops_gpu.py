@@ -534,6 +534,24 @@ def test_attend_extreme_scores():
     within(got[:4], want[:4], tol[:4], "beside a NaN")
 
 
+def test_attend_largest_f16_values_in_8_bits():
+    # 65504 is held as 256 times the scale 2^8: 65536, beyond f16
+    pool = Pool([200], 1, 64, 16, "f16", "fp8", 18)
+    pool.fill(19)
+    sign = (torch.arange(200) % 2 * 2 - 1).half()
+    k, v = rand(gen(20), 200, 1, 64, dtype="f16"), rand(gen(21), 200, 1, 64, dtype="f16")
+    k[:, 0, 0] = 65504 * sign
+    v[:, 0, 5] = 65504 * sign
+    v[::7, 0, 6] = -65504
+    pool.held = [(pool.put(pool.k, pool.ks, 0, k), pool.put(pool.v, pool.vs, 0, v))]
+    assert float(pool.held[0][0].max()) == 65536 == -float(pool.held[0][1].min())
+    q = rand(gen(22), 1, 2, 64, dtype="f16")
+    q[:, :, 0] = 2.0 ** -14
+    want, tol = attend_want(pool, q)
+    # values of a row whose scale is 2^8 are multiples of 2^-1: exact halved
+    within(attend(pool, q), want, tol, "65504")
+
+
 def test_attend_small_values_in_8_bits():
     # V of an fp8 cache far below f16's normal range times its scale
     pool = Pool([90], 1, 64, 16, "f16", "fp8", 18)
