@@ -72,9 +72,9 @@ __device__ __forceinline__ void store8(T* row, int j, int cols, const float (&f)
 }
 
 // A row in the registers of a workgroup's waves (LPR = 0), or of LPR = 16
-// lanes of one of four waves, each lane VPT pieces of eight values: every tensor is read or written
-// once, each place by one thread, which has read what H or Y may overwrite
-// there before it writes.  All loads, the weights'
+// lanes of one of four waves, each lane VPT pieces of eight values: every
+// tensor is read or written once, each place by one thread, which has read
+// what H or Y may overwrite there before it writes.  All loads, the weights'
 // included, are issued before anything waits, and the sum and an E4M3
 // output's largest |h w| (its scale needs only that times 1 / rms) cross the
 // waves together: one memory latency and one barrier a row.
@@ -135,17 +135,17 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void rmsnorm_rows(Args a) {
       }
     }
     const float rs = 1.0f / __builtin_sqrtf(ss / (float)a.cols + a.eps);
-    float f = rs;
+    float inv = 1.0f;  // (apart from rs: their product may overflow, for a tiny eps)
     if constexpr (FP8) {
       const float s = fmaxf(mx * rs / 448.0f, 0x1p-100f);
-      f = rs / s;
+      inv = 1.0f / s;
       if (at == 0) a.y_scale[row] = s;
     }
     TOut* yp = (TOut*)a.Y + row * a.ldy;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) h[i][u] *= f;
+      for (int u = 0; u < 8; ++u) h[i][u] = FP8 ? h[i][u] * rs * inv : h[i][u] * rs;
       store8<TOut, ANY>(yp, at + i * step, a.cols, h[i]);
     }
   }

@@ -40,7 +40,8 @@ extern "C" {
  * H and Y may each be X or R itself (same pointer and leading dimension; Y
  * only in format `dtype`); nothing else may overlap an output.
  * The sum of squares is an fp32 sum: a row holding an infinity or NaN, or
- * values whose squares overflow it, is normalised by that sum.
+ * values whose squares overflow it, is normalised by that sum.  h w is an
+ * fp32 product, formed before the division: where it overflows, so does y.
  * Any alignment of an element; 16-byte aligned pointers and leading
  * dimensions that are multiples of 8 take the fast path (W included).
  * rows = 0 does nothing.

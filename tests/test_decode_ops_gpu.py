@@ -157,6 +157,17 @@ def test_rmsnorm_values(cols, out):
         assert float(s[0]) == 2.0 ** -100
 
 
+def test_rmsnorm_eight_bits_of_zeros_and_a_tiny_eps():
+    # 1 / rms of a row of zeros is 1e15, over the least scale more than fp32
+    # holds
+    x = rand(gen(3), 3, 200)
+    x[1] = 0
+    w = torch.ones(200, dtype=torch.bfloat16)
+    _, y, s = rms_run(x, None, w, 1e-30, "bf16", "fp8", with_h=False)
+    assert bool((y[1].float() == 0).all()) and float(s[1]) == 2.0 ** -100
+    rms_check(x, None, w, 1e-30, "bf16", None, y, s, "tiny eps")
+
+
 def test_rmsnorm_many_short_rows():
     # the per-head norm of queries: many rows of 64, more rows than a grid's
     # first workgroups
