@@ -5,17 +5,21 @@
 // Two kernels.  `shrink` forms the inner products U = X A^T (rank values a
 // row) as fp32 partial sums over ranges of K; `expand` adds the partials in
 // their order, brings U to the input format in two parts and does the second
-// product for a range of columns.  Rows come in any order of adapters: a
-// workgroup takes 16 consecutive rows -- an MFMA operand -- and runs once
-// over each adapter that occurs among them, keeping of each product the rows
-// that are the adapter's; where tiles are few, the adapters of a tile are
-// spread over workgroups (grid z).
+// product for a range of columns.  Small problems take `expand` alone, which
+// then forms U itself.  Rows come in any order of adapters: a workgroup takes
+// 16 consecutive rows -- an MFMA operand -- and runs once over each adapter
+// that occurs among them, keeping of each product the rows that are the
+// adapter's; where tiles are few, the adapters of a tile are spread over
+// workgroups (grid z).
 //
-// Measured and not kept: both products in one kernel, U never leaving LDS
-// (4096 x 4096 -> 4096, rank 64: 48 us against 41, as all of A and B pass
-// through each CU); tiles of 32 rows (39 against 41 us, but 80 against 56
-// where each row has another adapter) and, for the second product, of 64;
-// B and R one and two turns ahead through a wave's columns (44 us).
+// Measured and not kept: both products of a large problem in one kernel (4096
+// x 4096 -> 4096, rank 64: 48 us against 41, as all of A and B pass through
+// each CU); tiles of 32 rows (39 against 41 us, but 80 against 56 where each
+// row has another adapter) and, for the second product, of 64; B and R one
+// and two turns ahead through a wave's columns (44 us); three or four
+// workgroups of `expand` a CU instead of two, by fewer registers and swizzled
+// instead of padded rows in LDS (42.8 and 65.9 against 43.7 us, few rows 10.2
+// against 8.6).
 #include "gemm_tile16.hpp"
 #include "wave.hpp"
 
@@ -58,7 +62,7 @@ __device__ __forceinline__ void each_adapter(int id, F&& f) {
   }
 }
 
-// U^T += A X^T over one of four waves' part of [kbeg, kend): first operand 16
+// U^T += A X^T over one of W waves' part of [kbeg, kend): first operand 16
 // of the adapter's rows, second the 16 rows of X, so that lane (m = l % 16, h
 // = l / 16) receives U[m][16 t + 4 h + e].  A wave's part is contiguous and
 // taken in stages of 64 columns.  Loads take whole cache lines, eight rows of
@@ -66,9 +70,10 @@ __device__ __forceinline__ void each_adapter(int id, F&& f) {
 // the L1 twice as long), and change lanes through the wave's own LDS: 16-byte
 // chunk x of row r at x ^ (r / 2 % 8), which keeps an operand's 16 rows on
 // different banks.  The next stage's loads are in flight while one is
-// multiplied.  The waves' parts and the tiles' first stages (`turn`) lie
+// multiplied (two or three more of them made it slower, 9.3 to 9.5 us for 16
+// rows, K = 4096 in one kernel).  The waves' parts and the tiles' first stages (`turn`) lie
 // apart, for the memory channels' sake.
-template <typename T, int RT>
+template <typename T, int RT, int W>
 __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0, int ad, int kbeg, int kend, char* lds,
                                       int wave, int lane, int turn) {
   const int lr = lane >> 3, lc = lane & 7, c = lane & 15, h = lane >> 4;
@@ -77,7 +82,7 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0,
   for (int j = 0; j < 2; ++j) x[j] = (const T*)a.X + (int64_t)min(row0 + 8 * j + lr, a.M - 1) * a.ldx + 8 * lc;
   const T* ab = (const T*)a.A + (int64_t)ad * a.rank * a.K;
   const uint32_t aoff = (uint32_t)lr * a.K + 8 * lc;
-  const int part = (kend - kbeg + 255) / 256 * 64;
+  const int part = (kend - kbeg + 64 * W - 1) / (64 * W) * 64;
   const int k1 = kbeg + part * wave, k2 = min(kend, k1 + part);
   const int stages = k2 > k1 ? (k2 - k1 + 63) / 64 : 0;
   if (stages == 0) return;
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(256) void shrink(Args a) {
   each_adapter(row_adapter(a, row0 + c), [&](int ad, uint32_t rows) {
     if (number++ % gridDim.z != blockIdx.z) return;
     f32x4 acc[RT] = {};
-    inner<T, RT>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
+    inner<T, RT, 4>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
     __syncthreads();  // every wave has read its operands: their place holds the sums
     float* red = (float*)(lds + wave * PER);
 #pragma unroll
@@ -190,9 +195,10 @@ __global__ __launch_bounds__(256) void shrink(Args a) {
 
 // The second product, C^T = B U^T: first operand 16 rows of B (columns of C),
 // second the 16 rows of U, so that lane (m, h) receives four columns of row m
-// per product.  A workgroup has 16 rows and 256 columns at a time, 64 a wave;
-// it adds up its rows' partials of U, eight values a thread, and leaves U's
-// two parts in LDS.  The 64 rows of B of a wave are contiguous and loaded so,
+// per product.  A workgroup has 16 rows and 64 columns a wave at a time; it
+// adds up its rows' partials of U, eight values a thread, and leaves U's two
+// parts in LDS.  ONE: no kernel before it, it forms U itself, its eight waves
+// each an eighth of K.  The 64 rows of B of a wave are contiguous and loaded so,
 // then change lanes through the wave's LDS; C changes lanes there too, so
 // that R and C move in whole lines, eight rows of 128 bytes an instruction.
 // The loads of the first columns are all issued before the first wait.
@@ -200,12 +206,14 @@ __global__ __launch_bounds__(256) void shrink(Args a) {
 // rows, the first also the rows without one.  PAST: R and C are more than the
 // caches hold and move past them.  Bound by R and C, and for small problems
 // by the chain of ids, U and the LDS's two turns.
-template <typename T, int RT, bool PAST>
-__global__ __launch_bounds__(256) void expand(Args a) {
+template <typename T, int RT, bool PAST, bool ONE>
+__global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
+  constexpr int W = ONE ? 8 : 4;  // waves
   constexpr int RP = 16 * RT, ST = (RP + 31) / 32, LD = RP + 8;
   constexpr int PIECES = RP / 8, BL = 2 * RT;  // of a row of U; of a lane in 64 rows of B
-  constexpr int PER = 64 * LD * 2 > 16 * 68 * 4 ? 64 * LD * 2 : 16 * 68 * 4;
-  __shared__ __attribute__((aligned(16))) char lds[4 * PER];
+  constexpr int PER2 = 64 * LD * 2 > 16 * 68 * 4 ? 64 * LD * 2 : 16 * 68 * 4;
+  constexpr int PER = ONE && (1 + RT) * 2048 > PER2 ? (1 + RT) * 2048 : PER2;
+  __shared__ __attribute__((aligned(16))) char lds[W * PER];
   __shared__ __attribute__((aligned(16))) uint16_t su[2][16][LD];
   __shared__ int sex[16], list[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -247,12 +255,35 @@ __global__ __launch_bounds__(256) void expand(Args a) {
       r[j] = PAST ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p;
     }
   };
-  const int step = gridDim.y * 256;
-  int n0 = (blockIdx.y * 4 + wave) * 64;
+  const int step = gridDim.y * 64 * W;
+  int n0 = (blockIdx.y * W + wave) * 64;
   load_b(first, min(n0, a.N - 1));  // (no adapter: the first one's, not used)
   load_r(n0);
   const float back = id >= 0 && a.scale ? a.scale[id] : 1.0f;
-  if (threadIdx.x < 16 * PIECES) {
+  if constexpr (ONE) {
+    // (at most one adapter: there is a workgroup for each)
+    f32x4 acc[RT] = {};
+    if (count > 0) inner<T, RT, W>(a, acc, row0, first, 0, a.K, wl, wave, lane, blockIdx.y);
+    float* red = (float*)wl;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[c * (RP + 1) + 16 * t + 4 * h + e] = acc[t][e];
+    __syncthreads();
+    if (threadIdx.x < 16 * PIECES) {
+      const int m = threadIdx.x / PIECES, x = threadIdx.x % PIECES * 8;
+      float u[8] = {};
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] += ((const float*)(lds + w * PER))[m * (RP + 1) + x + e];
+      u32x4 hi, lo;
+      const int ex = split<T, PIECES>(u, hi, lo);
+      *(u32x4*)&su[0][m][x] = hi;
+      *(u32x4*)&su[1][m][x] = lo;
+      if (x == 0) sex[m] = ex;
+    }
+  } else if (threadIdx.x < 16 * PIECES) {
     const int m = threadIdx.x / PIECES, x = threadIdx.x % PIECES * 8;
     float u[8] = {};
     if (x < a.rank && row0 + m < a.M && (mine >> m & 1)) {
@@ -358,8 +389,8 @@ __global__ __launch_bounds__(256) void expand(Args a) {
 }
 
 // Ranges of K, by the sizes alone.  Up to 1024 rows eight of 512 or more,
-// which give the chip work (K = N = 4096: 16 rows 8.7 us, one range 11.1; 512
-// rows, rank 64, 15.3 against 20.2); more rows one, as partial sums then cost
+// which give the chip work (K = N = 4096, two kernels: 16 rows 8.7 us, one
+// range 11.1; 512 rows, rank 64, 15.3 against 20.2); more rows one, as partial sums then cost
 // what the ranges gain (4096 rows, rank 64: 43.4 us, two 44.8, four 42.6; rank
 // 16 29.0, 29.0, 30.4).
 struct Cut {
@@ -376,12 +407,33 @@ inline Cut cut(int64_t M, int64_t K) {
 
 inline int64_t rank_pad(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
+// Both products in one kernel: each workgroup then reads its adapter's whole
+// A and its rows' whole X (`bytes`) by itself, against a second launch and
+// U's way through memory.  That pays up to 320 KiB a workgroup and rank 64 (16
+// rows, N = 4096: K = 1024, rank 16 6.7 us, two kernels 8.8; K = 2048, rank 64
+// 9.1 and 9.9; K = 4096, rank 16 9.2 and 8.6 on the GPU, but 3 us less of the
+// host; K = 4096, rank 64 12.7 and 9.5; K = 1024, rank 128 14.3 and 12.3),
+// while all workgroups run at once and read no more than 80 MiB together (128
+// rows, 512 workgroups, rank 16: K = 1024 8.9 and 11.5, K = 4096 13.3 and
+// 11.8).
+inline bool one(int64_t tiles, int64_t columns, int64_t adapters, int64_t bytes) {
+  const int64_t wgs = tiles * columns * adapters;
+  return bytes <= 320 << 10 && wgs <= 512 && wgs * bytes <= 80 << 20;
+}
+
 // Workgroups among which a tile's adapters are spread (grid z): as many as it
 // can hold where tiles are few.  Those that find no adapter of theirs end at
 // once; `expand`, whose rows cost more than its adapters, spreads less.
 template <typename T, int RT>
 hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
   const int most = min(a.adapters, min(a.M, 16));
+  if constexpr (RT <= 4) {
+    const int y = (a.N + 511) / 512;
+    if (one(s.tiles, y, most, (int64_t)(16 + 16 * RT) * a.K * 2)) {
+      hipLaunchKernelGGL((expand<T, RT, false, true>), dim3(s.tiles, y, most), dim3(512), 0, stream, a);
+      return hipGetLastError();
+    }
+  }
   const int z1 = s.tiles <= 4 ? most : s.tiles <= 256 ? min(most, 4) : 1;
   const int z2 = s.tiles <= 4 ? most : s.tiles <= 32 ? min(most, 4) : 1;
   hipLaunchKernelGGL((shrink<T, RT>), dim3(s.tiles, s.ksplit, z1), dim3(256), 0, stream, a);
@@ -392,9 +444,9 @@ hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
   // 4096, rank 16: 98 us against 111; 512 rows 16.7 against 15.7)
   const int y = min((a.N + 255) / 256, max(1, 1024 / s.tiles / z2));
   if ((int64_t)a.M * a.N * 4 > ((int64_t)32 << 20))
-    hipLaunchKernelGGL((expand<T, RT, true>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((expand<T, RT, true, false>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((expand<T, RT, false>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((expand<T, RT, false, false>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

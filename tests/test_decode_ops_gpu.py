@@ -243,6 +243,17 @@ def test_lora(M, N, K, rank, adapters, dtype):
         lora_check(*c, lora_run(*c, dtype, extra), dtype, f"{M}x{N}x{K} r{rank} extra {extra}")
 
 
+@pytest.mark.parametrize("M,N,K,rank,adapters", [
+    (20, 300, 8192, 32, 12), (64, 4096, 4096, 64, 6), (3, 40000, 1024, 16, 16), (16, 520, 10000, 8, 20), (48, 1030, 1440, 128, 4),
+    (1, 513, 2552, 16, 1), (2, 511, 1024, 64, 3), (128, 512, 1024, 16, 8), (16, 24, 8, 128, 2), (129, 1200, 520, 48, 4)])
+def test_lora_few_rows(M, N, K, rank, adapters):
+    # sizes on both sides of what one kernel and two are taken for
+    ids = [(m * 5 + m // 3) % (adapters + 1) - 1 for m in range(M)]
+    c = lora_case(M, N, K, rank, adapters, "bf16", ids, M + N + K)
+    for extra in (0, 8, 3):
+        lora_check(*c, lora_run(*c, "bf16", extra), "bf16", f"{M}x{N}x{K} r{rank} extra {extra}")
+
+
 @pytest.mark.parametrize("ids", ["same", "none", "runs", "each"])
 @pytest.mark.parametrize("residual,scale", [(True, False), (False, True)])
 @pytest.mark.parametrize("M", [80, 600])
