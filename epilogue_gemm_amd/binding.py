@@ -322,7 +322,7 @@ def _explain(name, t, dtype, shape, index, strided):
 
 def _rows2(name, t, dtype, shape, index):
     """Elements between the rows of a 2-d tensor with packed columns."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+    if t.dtype is not dtype or t.size() != shape or t.get_device() != index:
         _explain(name, t, dtype, shape, index, True)
     ld, one = t.stride()
     if one != 1 and shape[1] != 1:
@@ -332,7 +332,7 @@ def _rows2(name, t, dtype, shape, index):
 
 def _rows3(name, t, dtype, shape, index):
     """Elements between the rows of a 3-d tensor with packed rows."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+    if t.dtype is not dtype or t.size() != shape or t.get_device() != index:
         _explain(name, t, dtype, shape, index, True)
     ld, mid, one = t.stride()
     if (one != 1 and shape[2] != 1) or (mid != shape[2] and shape[1] != 1):
@@ -342,7 +342,7 @@ def _rows3(name, t, dtype, shape, index):
 
 def _packed(name, t, dtype, shape, index):
     """Address of a contiguous tensor."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not dtype or t.size() != shape or t.get_device() != index or not t.is_contiguous():
         _explain(name, t, dtype, shape, index, False)
     return t.data_ptr()
 
