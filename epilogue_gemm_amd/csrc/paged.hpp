@@ -60,6 +60,13 @@ GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 // one more.  A sequence's units in one column are then cut into pieces where
 // shares end.  No share is empty: of more workgroups than units the first F
 // take one each.
+// Workgroups that share F units: all of `most`, but where that is two for
+// each of 256 CUs, one each up to two units a workgroup (fewer pieces are
+// joined sooner: 1 x 8192 E4M3, 8 heads of 128, 512 units, 12.1 us with 256,
+// 15.1 with 512; 1 x 16384 16.6 and 19.9, but 4 x 8192 of mixed lengths, 1400
+// units, 23.7 and 22.4, 16 x 8192 44.1 and 36.7.  Not numbers between, which
+// leave some CUs two and others one: 64 x 1000 40.7 us, 512 32.7).
+GE_HD int workgroups_of(int F, int most) { return most > 256 && F <= 2 * most ? 256 : most; }
 struct Shares {
   int n, base, more;  // shares, numbers in each, and how many have one more
 };
@@ -78,7 +85,7 @@ GE_HD int share_of(Shares s, int f) {
 // that takes at most kRounds rounds of loads (a round: kBatch pieces for each
 // group of threads, a group being rows * head_dim / 4 of the 256), else by
 // the join kernel.
-constexpr int kBatch = 16, kRounds = 4;
+constexpr int kBatch = 16, kRounds = 5;
 GE_HD bool joined_here(int pieces, int rows, int head_dim) {
   const int most = 1024 / head_dim;  // rows at a time
   const int passes = (rows + most - 1) / most, groups = rows < most ? most / rows : 1;

@@ -5,7 +5,10 @@
 //
 // with the keys of all sequences and heads split evenly over the workgroups
 // that the chip holds at once (paged.hpp), and the pieces of a sequence that
-// the split cuts joined by a second kernel.
+// the split cuts joined by the workgroup that finishes last, or, where they
+// are many, by a second kernel.  Bound by the cache's bytes (32 x 8192 bf16
+// of mixed lengths, 8 heads of 128: 95 us, 5.5 TB/s), for few keys by the
+// chain of lookups, loads and the join (1 x 1000: 8.7 us, 3 of them the join).
 //
 // For each piece -- some keys of one sequence, one key head and up to 16 of
 // the query heads that share it -- the four waves of a workgroup take every
@@ -141,8 +144,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // Workgroups of the decode attention: those the memory system wants in flight
 // at once.  Rows of 256 bytes: one for each of the 256 CUs (its waves then
 // have 64 to 128 KiB in flight; 32 x 8192 bf16, D = 128: 96 us, two for each
-// 102); shorter rows: two (8 x 65536 E4M3, D = 128: 115 against 151 us; 128 x
-// 2047 f16, D = 64: 108 against 116).
+// 102); shorter rows: up to two (8 x 65536 E4M3, D = 128: 109 against 150 us;
+// 128 x 2047 f16, D = 64: 108 against 116).
 constexpr int kWorkgroups = 512;
 inline int workgroups_for(int row_bytes) { return row_bytes == 256 ? 256 : kWorkgroups; }
 static_assert(kWorkgroups * 4 == GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES, "a counter each");
@@ -328,7 +331,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = 0u;
     }
-  const Shares sh = make_shares(un.total * columns, gridDim.x);
+  const Shares sh = make_shares(un.total * columns, workgroups_of(un.total * columns, gridDim.x));
   if (w >= sh.n) return;
   int f = share_begin(sh, w);
   const int fend = share_begin(sh, w + 1);
@@ -636,7 +639,8 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
   for (int i = un.i0; i < un.i1 && i < seq; ++i) at += units_of(seq_len(a.lens[i], cap));
   const int begin = __builtin_amdgcn_readlane(at, seq / un.per);
   const int head = qhead / a.group, qg = qhead % a.group;
-  const Shares sh = make_shares(un.total * a.heads * a.qtiles, a.workgroups);
+  const int F = un.total * a.heads * a.qtiles;
+  const Shares sh = make_shares(F, workgroups_of(F, a.workgroups));
   const int f0 = un.total * (head * a.qtiles + qg / 16) + begin;
   const int w0 = share_of(sh, f0), pieces = share_of(sh, f0 + units - 1) - w0 + 1;
   if (pieces == 1 || joined_here(pieces, min(16, a.group - qg / 16 * 16), D)) return;

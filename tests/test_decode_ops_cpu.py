@@ -203,6 +203,7 @@ int c_units_of(int len) { return units_of(len); }
 int c_shares(int F, int n) { return make_shares(F, n).n; }
 int c_share_begin(int F, int n, int w) { return share_begin(make_shares(F, n), w); }
 int c_share_of(int F, int n, int f) { return share_of(make_shares(F, n), f); }
+int c_workgroups_of(int F, int most) { return workgroups_of(F, most); }
 int c_joined_here(int pieces, int rows, int d) { return joined_here(pieces, rows, d); }
 int64_t c_pieces_bound(int64_t cap, int columns, int n) { return pieces_bound(cap, columns, n); }
 }
@@ -307,3 +308,24 @@ def test_who_joins(paged):
             assert here[0] and here == sorted(here, reverse=True)
             if rows > 1:
                 assert all(a <= b for a, b in zip(here, [paged.c_joined_here(p, rows - 1, d) for p in range(1, 600)]))
+
+
+def test_workgroups_of_few_units(paged):
+    for most in (1, 100, 256, 300, 512):
+        n = [paged.c_workgroups_of(F, most) for F in (0, 1, 2047, 2048, 2056, 3000, 4096, 1 << 20, INT_MAX)]
+        assert all(1 <= x <= most for x in n) and n == sorted(n) and n[0] == min(most, 256) and n[-3:] == [most] * 3
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_pieces_of_few_units_stay_within_the_bound_for_all_workgroups(paged, seed):
+    # the host bounds the pieces by the most workgroups, the kernels may take fewer
+    rng = np.random.default_rng(200 + seed)
+    cap, columns = int(rng.choice([1000, 8192, 100000])), int(rng.choice([1, 2, 8, 30]))
+    units = [paged.c_units_of(int(n)) for n in rng.integers(0, cap + 1, size=int(rng.integers(1, 9)))]
+    F = sum(units) * columns
+    n, bound = paged.c_workgroups_of(F, 512), paged.c_pieces_bound(cap, columns, 512)
+    at = 0
+    for u in units:
+        if u:
+            assert paged.c_share_of(F, n, at + u - 1) - paged.c_share_of(F, n, at) + 1 <= bound
+        at += u
