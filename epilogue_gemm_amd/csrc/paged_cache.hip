@@ -379,16 +379,15 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   f32x4 acc[VEC] = {};
   float m = kNegInf, l = 0.0f;
   const int32_t* table = a.pages + seq * a.ld;
-  // the table's entries for the two groups of a tile (past the end: the
-  // tile's first, whose keys are then masked)
-  struct Pages {
-    int g[2];
-  };
-  auto pages_of = [&](int k0) __attribute__((always_inline)) {
-    Pages p;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) p.g[g] = table[divide((k0 + 16 * g < kend ? k0 + 16 * g : k0) >> 4, a.groups)];
-    return p;
+  // this wave's tiles are 128 keys apart
+  const int k1 = kbeg + 32 * wave, last = k1 < kend ? (kend - 1 - k1) / 128 : -1;
+  // The pages of 32 tiles at a time: lane 2 i + g has that of group g of the
+  // i-th (past the end: of the tile's first, whose keys are then masked).
+  // Looked up here, no tile's loads wait behind a lookup.
+  int entries = -1;
+  auto look_up = [&](int n) __attribute__((always_inline)) {
+    const int k = k1 + 128 * (n + (lane >> 1)), kg = k + 16 * (lane & 1);
+    entries = k < kend ? page_or_none(table[divide((kg < kend ? kg : k) >> 4, a.groups)], a.num_pages) : -1;
   };
   constexpr int CPR = RB / 16;  // chunks of a row
   auto kwrite = [&](int i) __attribute__((always_inline)) {
@@ -397,21 +396,27 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   };
   auto kread = [&](int i) __attribute__((always_inline)) { return c * RB + (((4 * i + h) ^ (c * RB / 256 % CPR)) << 4); };
   const uint32_t koff = (uint32_t)(16 * lane), voff = (uint32_t)(4 * h * D * EB + c * VEC * EB);
-  auto load = [&](Tl& t, int k0, Pages p) __attribute__((always_inline)) {
+  // Tile n of this wave; past the last one its first lines, which the loop
+  // below does not use (loads that are not always issued would make every wait
+  // a wait for all of them).
+  auto load = [&](Tl& t, int n) __attribute__((always_inline)) {
+    if (n <= last && n % 32 == 0) look_up(n);
+    const int i = min(n, last), k0 = k1 + 128 * i;
+    const uint32_t ko = n > last ? 0 : koff, vo = n > last ? 0 : voff;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int gk = k0 + 16 * g, at = gk < kend ? gk : k0;
-      const int page = page_or_none(p.g[g], a.num_pages);
+      const int page = __builtin_amdgcn_readlane(entries, 2 * (i & 31) + g);
       t.valid[g] = page < 0 ? 0 : max(0, min(kend - gk, 16));
       const int64_t row =
           row_of(max(page, 0), a.heads, head, a.page_size, at - divide(at >> 4, a.groups) * a.page_size);
       const char* kp = a.k + row * (D * EB);
       const char* vp = a.v + row * (D * EB);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) t.k[g][i] = __builtin_nontemporal_load((const u32x4*)(kp + koff + 1024 * i));
+      for (int i = 0; i < KL; ++i) t.k[g][i] = __builtin_nontemporal_load((const u32x4*)(kp + ko + 1024 * i));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const char* r = vp + voff + u * D * EB;
+        const char* r = vp + vo + u * D * EB;
         if constexpr (VW == 1) t.v[4 * g + u].x = *(const uint32_t*)r;
         else t.v[4 * g + u] = __builtin_nontemporal_load((const typename Tl::vwords*)r);
       }
@@ -523,24 +528,17 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       acc[j] = mfma16<T>(vf, pl, acc[j]);
     }
   };
-  // This wave's tiles are 128 keys apart.  The next tile's loads, and the
-  // table entries of the one after it, are in flight while one is
-  // multiplied; past the last tile they read it again (from the cache).
-  const int k1 = kbeg + 32 * wave;
-  if (k1 < kend) {
-    const int last = k1 + (kend - 1 - k1) / 128 * 128;
+  // The next tile's loads are in flight while one is multiplied.
+  if (last >= 0) {
     Tl t0, t1;
-    load(t0, k1, pages_of(k1));
-    Pages p = pages_of(min(k1 + 128, last));
-    for (int k0 = k1;; k0 += 256) {
-      load(t1, min(k0 + 128, last), p);
-      p = pages_of(min(k0 + 256, last));
+    load(t0, 0);
+    for (int n = 0;; n += 2) {
+      load(t1, n + 1);
       multiply(t0);
-      if (k0 + 128 > last) break;
-      load(t0, min(k0 + 256, last), p);
-      p = pages_of(min(k0 + 384, last));
+      if (n + 1 > last) break;
+      load(t0, n + 2);
       multiply(t1);
-      if (k0 + 256 > last) break;
+      if (n + 2 > last) break;
     }
   }
 
