@@ -62,10 +62,10 @@ GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 // take one each.
 // Workgroups that share F units: all of `most`, but where that is two for
 // each of 256 CUs, one each up to two units a workgroup (fewer pieces are
-// joined sooner: 1 x 8192 E4M3, 8 heads of 128, 512 units, 12.1 us with 256,
-// 15.1 with 512; 1 x 16384 16.6 and 19.9, but 4 x 8192 of mixed lengths, 1400
-// units, 23.7 and 22.4, 16 x 8192 44.1 and 36.7.  Not numbers between, which
-// leave some CUs two and others one: 64 x 1000 40.7 us, 512 32.7).
+// joined sooner: 16 x 1000 E4M3 of mixed lengths, 8 heads of 64, some 560
+// units, 12.7 us with 256, 15.6 with 512; 4 x 8192, 1400 units, 14.5 and
+// 13.7).  Not numbers between, which leave some CUs two and others one (64 x
+// 1000, D = 128, 40.7 us with 280 of them, 512 32.7).
 GE_HD int workgroups_of(int F, int most) { return most > 256 && F <= 2 * most ? 256 : most; }
 struct Shares {
   int n, base, more;  // shares, numbers in each, and how many have one more
