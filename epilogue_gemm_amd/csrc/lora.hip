@@ -15,11 +15,14 @@
 // Measured and not kept: both products of a large problem in one kernel (4096
 // x 4096 -> 4096, rank 64: 48 us against 41, as all of A and B pass through
 // each CU); tiles of 32 rows (39 against 41 us, but 80 against 56 where each
-// row has another adapter) and, for the second product, of 64; B and R one
-// and two turns ahead through a wave's columns (44 us); three or four
-// workgroups of `expand` a CU instead of two, by fewer registers and swizzled
-// instead of padded rows in LDS (42.8 and 65.9 against 43.7 us, few rows 10.2
-// against 8.6).
+// row has another adapter) and, for the second product, of 64; a second copy
+// of the second product's loop for whole rows of one adapter, the next columns'
+// loads in flight (41.8 against 43.6 us); eight waves a tile in the first
+// product (42.6 against 41.9 us, 17.2 against 15.4 for 512 rows); three or
+// four workgroups of `expand` a CU instead of two, by fewer registers and
+// swizzled instead of padded rows in LDS (42.8 and 65.9 against 43.7 us, few
+// rows 10.2 against 8.6); consecutive tiles on one XCD (16384 rows 112 against
+// 99 us, rank 16).
 #include "gemm_tile16.hpp"
 #include "wave.hpp"
 
