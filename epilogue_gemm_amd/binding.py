@@ -15,6 +15,7 @@ import re
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgemm_epi.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "gemm_epi.h")
 
 # Enum values of include/gemm_epi.h
@@ -302,67 +303,32 @@ def gemm_epi_attention_decode_workspace_size(cache, batch, width, q_heads) -> in
 ATTENTION_DECODE_COUNTER_BYTES = 2048  # GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES
 
 
-# What the tensor calls below check is cheap to compare and slow to explain:
-# they compare inline and come here only to say what was wrong.
+# The tensor calls below check their arguments and call the library in
+# _calls.so (torch_calls.cpp): 4.0 us a call, most of it the launch, where
+# checks written here and ctypes took 6.7.
 
-def _explain(name, t, dtype, shape, index, strided):
-    """Raises the ValueError that fits a tensor which is not a CUDA tensor of
-    this dtype and shape on device `index`, packed but for the first axis
-    where `strided`."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: on device {t.get_device()}, the current device is {index}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name}: only the first axis may be strided" if strided else f"{name}: expected a contiguous tensor")
+class _Calls:
+    """That module, and torch's current device and stream as plain numbers,
+    looked up at the first call."""
+    m = None
 
 
-def _rows2(name, t, dtype, shape, index):
-    """Elements between the rows of a 2-d tensor with packed columns."""
-    if t.dtype is not dtype or t.size() != shape or t.get_device() != index:
-        _explain(name, t, dtype, shape, index, True)
-    ld, one = t.stride()
-    if one != 1 and shape[1] != 1:
-        _explain(name, t, dtype, shape, index, True)
-    return ld if shape[0] != 1 else shape[1]  # one row has no distance to a next one
-
-
-def _rows3(name, t, dtype, shape, index):
-    """Elements between the rows of a 3-d tensor with packed rows."""
-    if t.dtype is not dtype or t.size() != shape or t.get_device() != index:
-        _explain(name, t, dtype, shape, index, True)
-    ld, mid, one = t.stride()
-    if (one != 1 and shape[2] != 1) or (mid != shape[2] and shape[1] != 1):
-        _explain(name, t, dtype, shape, index, True)
-    return ld if shape[0] != 1 else shape[1] * shape[2]
-
-
-def _packed(name, t, dtype, shape, index):
-    """Address of a contiguous tensor."""
-    if t.dtype is not dtype or t.size() != shape or t.get_device() != index or not t.is_contiguous():
-        _explain(name, t, dtype, shape, index, False)
-    return t.data_ptr()
-
-
-class _Torch:
-    """What the calls below use of torch, looked up at the first one."""
-    half = None  # torch.dtype -> format code of the 16-bit formats
-
-
-def _torch():
+def _load_calls():
     import torch
 
-    T = _Torch
-    T.torch, T.i32, T.f32, T.fp8 = torch, torch.int32, torch.float32, torch.float8_e4m3fn
-    T.device, T.raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if T.device is None or T.raw is None:
-        T.device, T.raw = torch.cuda.current_device, lambda index: torch.cuda.current_stream(index).cuda_stream
-    torch.cuda.current_device()  # (initialises the device)
     load_library()
-    T.half = {torch.float16: DTYPES["f16"], torch.bfloat16: DTYPES["bf16"]}
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"{CALLS_PATH} is missing: it is built beside the HIP library. "
+                           "Run `python -c 'import __graft_entry__ as g; g.build()'` or "
+                           "`python epilogue_gemm_amd/build.py` first.")
+    from . import _calls
+
+    C = _Calls
+    C.device, C.raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if C.device is None or C.raw is None:
+        C.device, C.raw = torch.cuda.current_device, lambda index: torch.cuda.current_stream(index).cuda_stream
+    torch.cuda.current_device()  # (initialises the device)
+    C.m = _calls
 
 
 def _stream_of(stream, index):
@@ -372,23 +338,16 @@ def _stream_of(stream, index):
     return stream.cuda_stream
 
 
-def _not_half(name, t):
-    raise ValueError(f"{name}: dtype {t.dtype}; expected float16 or bfloat16")
+def _workspace(nbytes, stream, zeros=0):
+    """A workspace from torch's allocator on the stream of the call, its first
+    `zeros` bytes zero."""
+    import torch
 
-
-def _workspace(workspace, need, index, stream, zeros=0):
-    """(pointer, bytes) of the caller's workspace, or of one of `need()` bytes,
-    the first `zeros` of them zero, from torch's allocator on the stream of
-    the call."""
-    if workspace is None:
-        torch = _Torch.torch
-        with torch.cuda.stream(stream):  # (None: the current one)
-            workspace = torch.empty(need(), dtype=torch.uint8, device="cuda")
-            if zeros:
-                workspace[:zeros].zero_()
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {index}")
-    return workspace.data_ptr(), workspace.nbytes
+    with torch.cuda.stream(stream):  # (None: the current one)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        if zeros:
+            workspace[:zeros].zero_()
+    return workspace
 
 
 def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e-6, stream=None):
@@ -398,30 +357,12 @@ def rmsnorm(x, weight, y, residual=None, residual_out=None, y_scale=None, eps=1e
     itself.  ``y`` is of the same format, or float8_e4m3fn with
     ``y_scale`` ([rows] float32) receiving each row's scale.  Enqueued on
     torch's current stream (or `stream`), not synchronised."""
-    T = _Torch
-    if T.half is None:
-        _torch()
-    index = T.device()
-    shape, dt = x.shape, x.dtype
-    if len(shape) != 2:
-        raise ValueError("x: expected a 2-d tensor [rows, cols]")
-    fmt = out = T.half[dt] if dt in T.half else _not_half("x", x)
-    rows, cols = shape
-    ldx, w = _rows2("x", x, dt, shape, index), _packed("weight", weight, dt, (cols,), index)
-    r = h = sc = None
-    ldr = ldh = 0
-    if residual is not None:
-        ldr, r = _rows2("residual", residual, dt, shape, index), residual.data_ptr()
-    if residual_out is not None:
-        ldh, h = _rows2("residual_out", residual_out, dt, shape, index), residual_out.data_ptr()
-    if y_scale is not None:
-        out, dt = 3, T.fp8  # DTYPES["fp8"]
-        sc = _packed("y_scale", y_scale, T.f32, (rows,), index)
-    ldy = _rows2("y", y, dt, shape, index)
-    if rows == 0:
-        return
-    st = _lib.gemm_epi_rmsnorm(x.data_ptr(), ldx, r, ldr, w, h, ldh, y.data_ptr(), ldy, sc, rows, cols, eps, fmt, out,
-                               T.raw(index) if stream is None else _stream_of(stream, index))
+    C = _Calls
+    if C.m is None:
+        _load_calls()
+    index = C.device()
+    st = C.m.rmsnorm(index, C.raw(index) if stream is None else _stream_of(stream, index), x, weight, y, residual,
+                     residual_out, y_scale, eps)
     if st != OK:
         raise GemmEpiError("gemm_epi_rmsnorm", st)
 
@@ -440,30 +381,14 @@ def lora(x, a, b, ids, c, scale=None, residual=None, workspace=None, stream=None
     ``workspace``: an optional CUDA tensor of ``lora_workspace_size`` bytes,
     else one is allocated.  With residual None, c is what ``Plan.run`` of the
     projection takes as its residual."""
-    T = _Torch
-    if T.half is None:
-        _torch()
-    index = T.device()
-    xs, sa, sb, dt = x.shape, a.shape, b.shape, x.dtype
-    if len(xs) != 2 or len(sa) != 3 or len(sb) != 3:
-        raise ValueError("x, a, b: expected tensors [M, K], [adapters, rank, K] and [adapters, N, rank]")
-    fmt = T.half[dt] if dt in T.half else _not_half("x", x)
-    (M, K), (adapters, rank, _), N = xs, sa, sb[1]
-    cs = (M, N)
-    ldx = _rows2("x", x, dt, xs, index)
-    pa, pb = _packed("a", a, dt, (adapters, rank, K), index), _packed("b", b, dt, (adapters, N, rank), index)
-    pi = _packed("ids", ids, T.i32, (M,), index)
-    ldc = _rows2("c", c, dt, cs, index)
-    ps = None if scale is None else _packed("scale", scale, T.f32, (adapters,), index)
-    pr, ldr = None, 0
-    if residual is not None:
-        ldr, pr = _rows2("residual", residual, dt, cs, index), residual.data_ptr()
-    if M == 0:
-        return
-    s = T.raw(index) if stream is None else _stream_of(stream, index)
-    ws, nbytes = _workspace(workspace, lambda: lora_workspace_size(M, N, K, rank, adapters), index, stream)
-    st = _lib.gemm_epi_lora(x.data_ptr(), ldx, pa, pb, ps, pi, pr, ldr, c.data_ptr(), ldc, M, N, K, rank, adapters, fmt,
-                            ws, nbytes, s)
+    C = _Calls
+    if C.m is None:
+        _load_calls()
+    index = C.device()
+    s = C.raw(index) if stream is None else _stream_of(stream, index)
+    st = C.m.lora(index, s, x, a, b, ids, c, scale, residual, workspace)
+    if st < 0:
+        st = C.m.lora(index, s, x, a, b, ids, c, scale, residual, _workspace(-st, stream))
     if st != OK:
         raise GemmEpiError("gemm_epi_lora", st)
 
@@ -491,47 +416,36 @@ class PagedCache:
         if fmt not in ("f16", "bf16", "fp8"):
             raise ValueError(f"k: dtype {k.dtype}; expected float16, bfloat16 or float8_e4m3fn")
         self.device_index = k.get_device()
-        pk = _packed("k", k, k.dtype, shape, self.device_index)
-        pv = _packed("v", v, k.dtype, shape, self.device_index)
+
+        def at(name, t, dtype, shape):
+            if not t.is_cuda or t.get_device() != self.device_index or t.dtype != dtype or t.shape != shape or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on k's device")
+            return t.data_ptr()
+
+        pk, pv = at("k", k, k.dtype, shape), at("v", v, k.dtype, shape)
         if (fmt == "fp8") != (k_scale is not None) or (fmt == "fp8") != (v_scale is not None):
             raise ValueError("k_scale, v_scale: for a float8_e4m3fn cache, and only then")
         pks = pvs = None
         if fmt == "fp8":
-            pks = _packed("k_scale", k_scale, torch.float32, shape[:3], self.device_index)
-            pvs = _packed("v_scale", v_scale, torch.float32, shape[:3], self.device_index)
+            pks = at("k_scale", k_scale, torch.float32, shape[:3])
+            pvs = at("v_scale", v_scale, torch.float32, shape[:3])
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = paged_cache_struct(pk, pv, pks, pvs, shape[0], shape[2], shape[1], shape[3], fmt)
-
-    def _table(self, pages, lens, index):
-        if index != self.device_index:
-            raise ValueError(f"the cache is on device {self.device_index}, the current device is {index}")
-        shape = pages.shape
-        if len(shape) != 2:
-            raise ValueError("pages: expected a 2-d tensor [batch, width]")
-        batch, width = shape
-        i32 = _Torch.i32
-        return _PageTable(pages.data_ptr(), _rows2("pages", pages, i32, shape, index), width,
-                          _packed("lens", lens, i32, (batch,), index), batch), batch
+        self._address = ctypes.addressof(self._struct)
 
     def append(self, k, v, pages, lens, starts=None, stream=None):
         """Writes the rows k and v [tokens, heads, head_dim] (rows may be
         strided) to their sequences' last positions.  ``starts`` [batch + 1]
         int32: the rows of sequence i are starts[i] .. starts[i + 1] - 1, rows
         from starts[batch] on are ignored; None: one row a sequence."""
-        T = _Torch
-        if T.half is None:
-            _torch()
-        index = T.device()
-        table, batch = self._table(pages, lens, index)
-        dt = k.dtype
-        fmt = T.half[dt] if dt in T.half else _not_half("k", k)
-        tokens = k.shape[0]
-        shape = (tokens, self.heads, self.head_dim)
-        ldk, ldv = _rows3("k", k, dt, shape, index), _rows3("v", v, dt, shape, index)
-        p = None if starts is None else _packed("starts", starts, T.i32, (batch + 1,), index)
-        st = _lib.gemm_epi_cache_append(self._struct, table, k.data_ptr(), ldk, v.data_ptr(), ldv, p, tokens, fmt,
-                                        T.raw(index) if stream is None else _stream_of(stream, index))
+        C = _Calls
+        if C.m is None:
+            _load_calls()
+        index = C.device()
+        st = C.m.append(index, C.raw(index) if stream is None else _stream_of(stream, index), self._address,
+                        self.device_index, k, v, pages, lens, starts)
         if st != OK:
             raise GemmEpiError("gemm_epi_cache_append", st)
 
@@ -547,26 +461,15 @@ class PagedCache:
         ``workspace_size`` bytes, its first ATTENTION_DECODE_COUNTER_BYTES
         zero before its first use (every completed run leaves them zero), else
         one is allocated."""
-        T = _Torch
-        if T.half is None:
-            _torch()
-        index = T.device()
-        table, batch = self._table(pages, lens, index)
-        dt = q.dtype
-        fmt = T.half[dt] if dt in T.half else _not_half("q", q)
-        shape = q.shape
-        if len(shape) != 3:
-            raise ValueError("q: expected a 3-d tensor [batch, q_heads, head_dim]")
-        heads = shape[1]
-        shape = (batch, heads, self.head_dim)
-        ldq, ldo = _rows3("q", q, dt, shape, index), _rows3("o", o, dt, shape, index)
-        if batch == 0:
-            return
-        s = T.raw(index) if stream is None else _stream_of(stream, index)
-        ws, nbytes = _workspace(workspace, lambda: self.workspace_size(heads, pages), index, stream,
-                                ATTENTION_DECODE_COUNTER_BYTES)
-        st = _lib.gemm_epi_attention_decode(self._struct, table, q.data_ptr(), ldq, o.data_ptr(), ldo, heads, fmt, ws,
-                                            nbytes, s)
+        C = _Calls
+        if C.m is None:
+            _load_calls()
+        index = C.device()
+        s = C.raw(index) if stream is None else _stream_of(stream, index)
+        args = (self._address, self.device_index, q, o, pages, lens)
+        st = C.m.attend(index, s, *args, workspace)
+        if st < 0:
+            st = C.m.attend(index, s, *args, _workspace(-st, stream, ATTENTION_DECODE_COUNTER_BYTES))
         if st != OK:
             raise GemmEpiError("gemm_epi_attention_decode", st)
 

@@ -1,8 +1,9 @@
 """Build the HIP library libgemm_epi.so for gfx950, in-tree.
 
 Every .hip/.cpp file under csrc/ is compiled by hipcc for gfx950 only, in
-parallel, then linked into epilogue_gemm_amd/libgemm_epi.so.  build()
-recompiles everything by default (it is the "does it build" check);
+parallel, then linked into epilogue_gemm_amd/libgemm_epi.so; torch_calls.cpp,
+the host-only module that checks torch tensors for binding.py, is compiled by
+g++ into _calls.so against the Python and torch headers.  build() recompiles everything by default (it is the "does it build" check);
 build(incremental=True) (``python -m epilogue_gemm_amd.build --incremental``)
 recompiles only the sources whose object is older than the source or any
 header it includes (from the compiler's dependency files).
@@ -11,14 +12,18 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgemm_epi.so")
+CALLS_SRC = os.path.join(HERE, "torch_calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -74,6 +79,20 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    """_calls.so; it finds the library beside itself, and torch's libraries
+    loaded (binding.py imports torch first)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-isystem", os.path.join(torch, "include"),
+           "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp, "-L", HERE, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(jobs: int | None = None, verbose: bool = False, incremental: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -90,8 +109,9 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_calls()
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources")
+        print(f"built {LIB} from {len(srcs)} sources, {CALLS}")
     return LIB
 
 

@@ -329,3 +329,19 @@ def test_pieces_of_few_units_stay_within_the_bound_for_all_workgroups(paged, see
         if u:
             assert paged.c_share_of(F, n, at + u - 1) - paged.c_share_of(F, n, at) + 1 <= bound
         at += u
+
+
+def test_tensor_calls_refuse_what_is_not_a_cuda_tensor():
+    # the host-only module's own checks; the device's index and stream are not used before them
+    torch = pytest.importorskip("torch")
+    gb.load_library()
+    from epilogue_gemm_amd import _calls
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    t = torch.zeros(2, 8, 8, dtype=torch.bfloat16)
+    for f, args in ((_calls.rmsnorm, (x, x[0], x, None, None, None, 1e-6)), (_calls.rmsnorm, (1, x[0], x, None, None, None, 1e-6)),
+                    (_calls.rmsnorm, (x[0], x[0], x, None, None, None, 1e-6)), (_calls.rmsnorm, (x.float(), x[0], x, None, None, None, 1e-6)),
+                    (_calls.lora, (x, t, t, x, x, None, None, None)), (_calls.lora, (x, x, t, x, x, None, None, None))):
+        with pytest.raises(ValueError):
+            f(0, 0, *args)
+    with pytest.raises(TypeError):
+        _calls.attend(0, 0)
