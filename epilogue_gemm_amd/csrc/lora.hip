@@ -443,8 +443,9 @@ hipError_t launch(const Args& a, const Cut& s, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // columns of a workgroup: 256, or more where that still leaves some 1024
-  // workgroups; R and C beyond the L2s' 32 MiB go past the caches (16384 x
-  // 4096, rank 16: 98 us against 111; 512 rows 16.7 against 15.7)
+  // workgroups; R and C beyond the L2s' 32 MiB go past the caches (4096 x 4096,
+  // rank 64: 43.7 us against 48.8, with a reading of C after it 49.8 against
+  // 54.8; 512 rows 16.7 against 15.7)
   const int y = min((a.N + 255) / 256, max(1, 1024 / s.tiles / z2));
   if ((int64_t)a.M * a.N * 4 > ((int64_t)32 << 20))
     hipLaunchKernelGGL((expand<T, RT, true, false>), dim3(s.tiles, y, z2), dim3(256), 0, stream, a);

@@ -5,7 +5,10 @@
 // per row, in fp32; h and y rounded once, y optionally to E4M3 with the
 // row's scale max|y| / 448.  HBM-bound for many rows (x and r read, h and y
 // written, once each), bound by one launch and one reduction's latency for
-// few.
+// few (16384 x 8192 bf16 with a residual 178 us, 6.0 TB/s; 8191 x 5120 f16 to
+// E4M3 26.7 us; 4 x 4096 2.7 us).  Storing past the caches was faster alone and
+// not kept, as the reader that follows pays for it (8192 x 5120 to E4M3 26.6
+// against 23.0 us, with a reading of y 33.4 against 34.6).
 #include "kernels.hpp"
 #include "wave.hpp"
 
