@@ -557,40 +557,37 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) so[wave][c][VEC * (4 * h + e) + j] = acc[j][e];
   __syncthreads();
-  const int qh = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * VEC;
-  if (first + qh < a.group) {
+  const int rows = min(16, a.group - first);
+  for (int p = threadIdx.x; p < rows * (D / 2); p += 256) {  // two values each
+    const int qh = p / (D / 2), d = p % (D / 2) * 2;
     const float mj = fmaxf(fmaxf(sm[0][qh], sm[1][qh]), fmaxf(sm[2][qh], sm[3][qh]));
     const float ref = mj == kNegInf ? 0.0f : mj;
-    float o[VEC] = {}, lj = 0.0f;
+    float o0 = 0.0f, o1 = 0.0f, lj = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = __builtin_amdgcn_exp2f(sm[i][qh] - ref);
       lj += x * sl[i][qh];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] += x * so[i][qh][d0 + j];
+      o0 += x * so[i][qh][d];
+      o1 += x * so[i][qh][d + 1];
     }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) o[j] *= 1.0f / kHalf;
+    o0 *= 1.0f / kHalf;
+    o1 *= 1.0f / kHalf;
     if (take == units) {
       const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
-      T* op = (T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d0;
-#pragma unroll
-      for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = pack2_out<T>(o[j] * inv, o[j + 1] * inv);
+      *(uint32_t*)((T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d) = pack2_out<T>(o0 * inv, o1 * inv);
     } else {
       // (agent-scope stores reach the level that all XCDs share)
+      auto store = [](float* to, float x, float y) __attribute__((always_inline)) {
+        __hip_atomic_store((uint64_t*)to, (uint64_t)__builtin_bit_cast(uint32_t, x) | (uint64_t)__builtin_bit_cast(uint32_t, y) << 32,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      };
       float* pp = part_of<D>(a, w, u == begin);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        __hip_atomic_store(pp + qh * D + d0 + j, o[j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (d0 == 0) {
-        __hip_atomic_store(pp + 16 * D + 2 * qh, mj, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(pp + 16 * D + 2 * qh + 1, lj, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      store(pp + qh * D + d, o0, o1);
+      if (d == 0) store(pp + 16 * D + 2 * qh, mj, lj);
     }
   }
   const int f0 = f - (u - begin);
   const int w0 = share_of(sh, f0), pieces = take == units ? 1 : share_of(sh, f0 + units - 1) - w0 + 1;
-  const int rows = min(16, a.group - first);
   if (take != units && joined_here(pieces, rows, D)) {
     // Count the piece at the sequence's counter (that of the workgroup in
     // whose share it begins: a share holds the beginning of at most one cut
