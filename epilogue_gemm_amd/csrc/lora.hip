@@ -42,8 +42,10 @@ struct Args {
   int64_t ldx, ldr, ldc;
   int M, N, K, rank, adapters;
   int ksplit, kper;  // ranges of K, and their length
-  bool vec;          // C and R by 16-byte accesses
 };
+
+// (a 16-byte access off its alignment is one instruction all the same)
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // The adapter of a row, -1 for none.
 __device__ __forceinline__ int row_adapter(const Args& a, int row) {
@@ -248,14 +250,15 @@ __global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
 #pragma unroll
     for (int i = 0; i < BL; ++i) b[i] = *(const u32x4*)(p + 8 * min(lane + 64 * i, most));
   };
-  // R's rows 8 j + lr; for a row that is not ours, one that is
+  // R's rows 8 j + lr (for a row that is not ours, one that is; the columns
+  // behind the last whole eight are read one by one below)
   auto load_r = [&](int n) __attribute__((always_inline)) {
-    if (!a.R || !a.vec || n + 64 > a.N) return;
+    if (!a.R || a.N < 8) return;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int m = mine >> (8 * j + lr) & 1 ? 8 * j + lr : __builtin_ctz(mine);
-      const T* p = (const T*)a.R + (int64_t)min(row0 + m, a.M - 1) * a.ldr + n + 8 * lc;
-      r[j] = PAST ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p;
+      const T* p = (const T*)a.R + (int64_t)min(row0 + m, a.M - 1) * a.ldr + min(n + 8 * lc, a.N - 8);
+      r[j] = PAST ? __builtin_nontemporal_load((const u32x4_any*)p) : *(const u32x4_any*)p;
     }
   };
   const int step = gridDim.y * 64 * W;
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
       const int row = row0 + 8 * j + lr, n = n0 + 8 * lc;
       if (row >= a.M || !(mine >> (8 * j + lr) & 1)) continue;
       T* cp = (T*)a.C + (int64_t)row * a.ldc + n;
-      if (a.vec && n0 + 64 <= a.N) {
+      if (n + 8 <= a.N) {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -375,8 +378,8 @@ __global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
           w[e] = pack2_out<T>(v[2 * e] + to_f32(__builtin_bit_cast(T, (uint16_t)(x & 0xffffu))),
                               v[2 * e + 1] + to_f32(__builtin_bit_cast(T, (uint16_t)(x >> 16))));
         }
-        if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4*)cp);
-        else *(u32x4*)cp = w;
+        if constexpr (PAST) __builtin_nontemporal_store(w, (u32x4_any*)cp);
+        else *(u32x4_any*)cp = w;
       } else {
         const T* rp = a.R ? (const T*)a.R + (int64_t)row * a.ldr + n : nullptr;
         for (int e = 0; e < 8; ++e)
@@ -505,10 +508,9 @@ gemm_epi_status gemm_epi_lora(const void* X, int64_t ldx, const void* A, const v
     return GEMM_EPI_ERR_UNSUPPORTED;
   if (workspace_bytes < ge::lora::workspace_bytes(M, K, rank)) return GEMM_EPI_ERR_INVALID_ARG;
   const ge::lora::Cut cut = ge::lora::cut(M, K);
-  const bool vec = (((uintptr_t)C | (uintptr_t)R) & 15u) == 0 && ldc % 8 == 0 && (!R || ldr % 8 == 0);
   const ge::lora::Args a{X,   A,   B,   R,      scale,  ids,       C,           (float*)workspace,
                          ldx, ldr, ldc, (int)M, (int)N, (int)K,    (int)rank,   (int)adapters,
-                         cut.ksplit, cut.kper, vec};
+                         cut.ksplit, cut.kper};
   const hipError_t e = dtype == GEMM_EPI_F16 ? ge::lora::launch_rank<ge::f16>(a, cut, (hipStream_t)stream)
                                              : ge::lora::launch_rank<ge::bf16>(a, cut, (hipStream_t)stream);
   if (e != hipSuccess) {
