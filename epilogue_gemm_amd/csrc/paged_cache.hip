@@ -7,8 +7,8 @@
 // that the chip holds at once (paged.hpp), and the pieces of a sequence that
 // the split cuts joined by the workgroup that finishes last, or, where they
 // are many, by a second kernel.  Bound by the cache's bytes (32 x 8192 bf16
-// of mixed lengths, 8 heads of 128: 92 us, 5.7 TB/s), for few keys by the
-// chain of lookups, loads and the join (1 x 1000: 8.4 us, 3 of them the join).
+// of mixed lengths, 8 heads of 128: 89 us, 5.9 TB/s), for few keys by the
+// chain of lookups, loads and the join (1 x 1000: 8.3 us, 3 of them the join).
 //
 // For each piece -- some keys of one sequence, one key head and up to 16 of
 // the query heads that share it -- the four waves of a workgroup take every
@@ -144,11 +144,10 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 // ---------------------------------------------------------------------------
 // Workgroups of the decode attention: those the memory system wants in flight
 // at once.  Rows of 128 bytes and more: one for each of the 256 CUs (its waves
-// then have 32 to 128 KiB in flight; 32 x 8192 bf16, D = 128: 92 us, two for
-// each 94; 8 x 65536 E4M3, D = 128: 102 and 105; 64 x 4000 f16, D = 64: 52 and
-// 54); shorter rows: up to two (16 x 16384 E4M3, D = 64: 30 against 34 us).
-// A third tile in flight was no faster (93 us; 109 against 107, 100 against
-// 97).
+// then have 32 to 128 KiB in flight; 1 x 131072 bf16, D = 128: 89 us, two for
+// each 95; 8 x 65536 E4M3, D = 128: 100 and 102; 32 x 8192 and 128 x 2047 f16, D
+// = 64, the same); shorter rows: up to two (16 x 32768 E4M3, D = 64: 53 against
+// 60 us).  A third tile in flight was no faster.
 constexpr int kWorkgroups = 512;
 inline int workgroups_for(int row_bytes) { return row_bytes >= 128 ? 256 : kWorkgroups; }
 static_assert(kWorkgroups * 4 == GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES, "a counter each");
