@@ -3,7 +3,8 @@
 Every .hip/.cpp file under csrc/ is compiled by hipcc for gfx950 only, in
 parallel, then linked into epilogue_gemm_amd/libgemm_epi.so; torch_calls.cpp,
 the host-only module that checks torch tensors for binding.py, is compiled by
-g++ into _calls.so against the Python and torch headers.  build() recompiles everything by default (it is the "does it build" check);
+g++ into _calls.so against the Python and torch headers.  build() recompiles
+everything by default (it is the "does it build" check);
 build(incremental=True) (``python -m epilogue_gemm_amd.build --incremental``)
 recompiles only the sources whose object is older than the source or any
 header it includes (from the compiler's dependency files).

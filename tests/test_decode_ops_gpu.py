@@ -505,6 +505,19 @@ def test_attend_one_workspace_for_calls_of_any_sizes():
         assert int(ws[:gb.ATTENTION_DECODE_COUNTER_BYTES].count_nonzero()) == 0
 
 
+def test_attend_more_tiles_than_one_lookup():
+    # 34 units a workgroup, so 34 tiles a wave, whose pages are looked up 32
+    # tiles at a time; some pages missing
+    pool = Pool([70000], 16, 64, 16, "bf16", "bf16", 41)
+    pool.table[0, 1500::211] = -1
+    g = torch.Generator(device="cuda").manual_seed(42)
+    k, v = (torch.randn(70000, 16, 64, generator=g, device="cuda").bfloat16().cpu() for _ in range(2))
+    pool.held = [(pool.put(pool.k, None, 0, k), pool.put(pool.v, None, 0, v))]
+    q = rand(gen(43), 1, 16, 64, std=2.0)
+    want, tol = attend_want(pool, q)
+    within(attend(pool, q), want, tol, "two lookups")
+
+
 def test_attend_missing_pages():
     # pages that do not exist at the front, in the middle, at the end, all of
     # them; entries past the cache and of the lowest value
