@@ -56,10 +56,12 @@ GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 // The keys of a batch are split evenly over its workgroups: with U the units
 // of all sequences and `columns` the (key head, query tile) pairs, unit u of
 // column c has number f = c U + u, of F = columns * U < 2^31 numbers, and each
-// workgroup takes a share of consecutive ones: F / n each, the first F % n
-// one more.  A sequence's units in one column are then cut into pieces where
-// shares end.  No share is empty: of more workgroups than units the first F
-// take one each.
+// of n workgroups takes a share of consecutive ones, from floor(w F / n) on.  A
+// sequence's units in one column are then cut into pieces where shares end.
+// No share is empty: of more workgroups than units the first F take one each.
+// The larger shares lie evenly among the others, so that any k consecutive ones
+// hold more than k F / n - 1 numbers (all of them first would leave the last
+// columns to the smaller ones, up to twice as many pieces: pieces_bound).
 // Workgroups that share F units: all of `most`, but where that is two for
 // each of 256 CUs, one each up to two units a workgroup (fewer pieces are
 // joined sooner: 16 x 1000 E4M3 of mixed lengths, 8 heads of 64, some 560
@@ -74,11 +76,14 @@ GE_HD Shares make_shares(int F, int workgroups) {
   const int n = F < workgroups ? F : workgroups;
   return n == 0 ? Shares{0, 0, 0} : Shares{n, (int)((uint32_t)F / (uint32_t)n), (int)((uint32_t)F % (uint32_t)n)};
 }
-GE_HD int share_begin(Shares s, int w) { return w * s.base + (w < s.more ? w : s.more); }
-// The share that has number f < F.
+// floor(w F / n), with F = n base + more (n below 2^16).
+GE_HD int share_begin(Shares s, int w) { return w * s.base + (int)((uint32_t)(w * s.more) / (uint32_t)s.n); }
+// The share that has number f < F: f n / F in fp32 is within one of it, as
+// every rounding is at most 2^-24 of a number of at most n.
 GE_HD int share_of(Shares s, int f) {
-  const uint32_t base = (uint32_t)s.base, big = (uint32_t)s.more * (base + 1);
-  return (uint32_t)f < big ? (int)((uint32_t)f / (base + 1)) : s.more + (int)(((uint32_t)f - big) / base);
+  const int at = (int)((float)f * ((float)s.n / ((float)s.base * (float)s.n + (float)s.more)));
+  const int w = at < s.n ? at : s.n - 1;
+  return w + (w + 1 < s.n && share_begin(s, w + 1) <= f) - (share_begin(s, w) > f);
 }
 
 // The pieces of a cut sequence are joined by the last of its workgroups when
@@ -92,7 +97,10 @@ GE_HD bool joined_here(int pieces, int rows, int head_dim) {
   return passes * ((pieces + kBatch * groups - 1) / (kBatch * groups)) <= kRounds;
 }
 // The most pieces a sequence of up to `cap` tokens can be cut into: one per
-// unit, and one per share of a column and the two it ends in.
+// unit, and one per share of a column and the two it ends in.  (The inner p - 2
+// of its p shares are whole, and the outer two have a unit of it at least: of the
+// U = F / columns units it can have, (p - 2) F / n - 1 < U - 2, and so p - 2 < n /
+// columns, for every n up to `workgroups`.)
 GE_HD int64_t pieces_bound(int64_t cap, int columns, int workgroups) {
   const int64_t units = (cap + kUnit - 1) / kUnit, shares = workgroups / columns + 2;
   return units < shares ? units : shares;

@@ -1,0 +1,74 @@
+"""The decode operators' index arithmetic (csrc/paged.hpp) over whole ranges of
+sizes, compiled for the host with the checks for undefined behaviour on."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def compiled(tmp_path, text):
+    src, so = tmp_path / "wrap.cpp", tmp_path / "wrap.so"
+    src.write_text('#include "paged.hpp"\nusing namespace ge::paged;\nextern "C" {\n' + text + "\n}\n")
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+                        "-static-libubsan", "-shared", "-fPIC", "-I", os.path.join(ROOT, "epilogue_gemm_amd", "csrc"),
+                        str(src), "-o", str(so)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return ctypes.CDLL(str(so))
+
+
+@pytest.mark.parametrize("most", [256, 512])
+def test_every_cut_sequence_is_joined(tmp_path, most):
+    # One sequence of U units in each of `columns` columns (the batch whose
+    # sequences are cut into the most pieces), all columns, and tables of its
+    # length and wider: the pieces stay within the host's bound, so a join
+    # that the main kernel leaves is one that the host launches.
+    lib = compiled(tmp_path, r'''
+    int sweep(int most, int columns, int units, int* at) {
+      for (int U = 1; U <= units; ++U)
+        for (int wide = 0; wide < 2; ++wide) {
+          const int64_t cap = wide ? 1 << 22 : (int64_t)U * kUnit, full = cap / kUnit * columns;
+          const int wgs = full < most ? (int)full : most, F = U * columns;
+          const Shares s = make_shares(F, workgroups_of(F, wgs));
+          const int bound = (int)pieces_bound(cap, columns, wgs);
+          for (int c = 0; c < columns; ++c) {
+            const int pieces = share_of(s, c * U + U - 1) - share_of(s, c * U) + 1;
+            bool left = pieces > bound;
+            for (int rows = 1; rows <= 16; ++rows)
+              for (int d = 64; d <= 128; d += 64)
+                left = left || (joined_here(bound, rows, d) && !joined_here(pieces, rows, d));
+            if (left) {
+              at[0] = U; at[1] = c; at[2] = pieces; at[3] = bound;
+              return 1;
+            }
+          }
+        }
+      return 0;
+    }''')
+    at = (ctypes.c_int * 4)()
+    for columns in range(1, 65):
+        assert lib.sweep(most, columns, 600, at) == 0, (columns, "units, column, pieces, bound", list(at))
+
+
+def test_shares_are_even_and_every_number_is_in_its_own(tmp_path):
+    # floor(w F / n) exactly, and the share of every number, for all small F
+    # and at the largest
+    lib = compiled(tmp_path, r'''
+    int sweep(int from, int to, int given) {
+      for (int F = from;; ++F) {
+        const Shares s = make_shares(F, given);
+        if (s.n != (F < given ? F : given)) return F;
+        for (int w = 0; w < s.n; ++w) {
+          const int a = share_begin(s, w), b = share_begin(s, w + 1);
+          if (a != (int)((int64_t)w * F / s.n) || b <= a || b - a - s.base > 1) return F;
+          if (share_of(s, a) != w || share_of(s, b - 1) != w || share_of(s, a + (b - a) / 2) != w) return F;
+        }
+        if (share_begin(s, s.n) != F) return F;
+        if (F == to) return 0;
+      }
+    }''')
+    for given in (1, 2, 3, 100, 255, 256, 257, 509, 511, 512):
+        for start, to in ((1, 3000), ((1 << 24) - 100, (1 << 24) + 100), ((1 << 30) - 100, (1 << 30) + 100), ((1 << 31) - 300, (1 << 31) - 1)):
+            assert lib.sweep(start, to, given) == 0, (start, given)

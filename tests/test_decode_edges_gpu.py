@@ -1,0 +1,34 @@
+"""The decode operators on the GPU at sizes and values beyond those of
+test_decode_ops_gpu.py, whose definitions in 64 bits and derived tolerances
+they share."""
+import pytest
+import torch
+
+from epilogue_gemm_amd import binding as gb
+from tests.test_decode_ops_gpu import Pool, attend, attend_want, gen, rand, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gb.load_library()
+
+
+@pytest.mark.parametrize("lens,heads,group,head_dim,dtype,cache", [
+    # one long sequence, or a few, cut into some one unit a workgroup: as many
+    # pieces as units in every column, the last ones too
+    ([10300], 4, 7, 128, "bf16", "bf16"), ([12000], 4, 8, 128, "f16", "fp8"), ([20600], 2, 4, 128, "bf16", "bf16"),
+    ([20600], 2, 7, 64, "f16", "f16"), ([10500], 4, 16, 64, "bf16", "bf16"), ([21000], 8, 16, 64, "bf16", "fp8"),
+    ([4200], 12, 16, 128, "f16", "f16"), ([9000], 1, 160, 128, "bf16", "bf16"), ([11000, 300, 0, 7], 4, 8, 128, "bf16", "bf16"),
+    ([6000, 6000], 4, 5, 128, "bf16", "fp8"),
+])
+@pytest.mark.parametrize("wide", [1, 4])
+def test_attend_writes_every_head_of_long_sequences(lens, heads, group, head_dim, dtype, cache, wide):
+    pool = Pool(lens, heads, head_dim, 64, dtype, cache, 80, width=wide * -(-max(lens) // 64))
+    pool.fill(81)
+    q = rand(gen(82), len(lens), heads * group, head_dim, std=1.5, dtype=dtype)
+    want, tol = attend_want(pool, q)
+    within(attend(pool, q), want, tol, f"{lens} {heads}x{group}")
