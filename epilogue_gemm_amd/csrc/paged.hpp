@@ -86,6 +86,16 @@ GE_HD int share_of(Shares s, int f) {
   return w + (w + 1 < s.n && share_begin(s, w + 1) <= f) - (share_begin(s, w) > f);
 }
 
+// A wave's tiles of 32 keys are 128 keys apart, from key k1 on; tile `last` is its
+// last one before kend.  The key whose page is looked up for one of the two
+// groups of 16 of a tile: past the sequence's end the tile's first, past the last
+// tile -1 (by the tile's number: near 2^31 the keys of tiles past it are no ints).
+GE_HD int looked_up_key(int k1, int kend, int last, int tile, int group) {
+  if (tile > last) return -1;
+  const int k = k1 + 128 * tile;
+  return kend - k > 16 * group ? k + 16 * group : k;
+}
+
 // The pieces of a cut sequence are joined by the last of its workgroups when
 // that takes at most kRounds rounds of loads (a round: kBatch pieces for each
 // group of threads, a group being rows * head_dim / 4 of the 256), else by

@@ -388,8 +388,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   // Looked up here, no tile's loads wait behind a lookup.
   int entries = -1;
   auto look_up = [&](int n) __attribute__((always_inline)) {
-    const int k = k1 + 128 * (n + (lane >> 1)), kg = k + 16 * (lane & 1);
-    entries = k < kend ? page_or_none(table[divide((kg < kend ? kg : k) >> 4, a.groups)], a.num_pages) : -1;
+    const int k = looked_up_key(k1, kend, last, n + (lane >> 1), lane & 1);
+    entries = k >= 0 ? page_or_none(table[divide(k >> 4, a.groups)], a.num_pages) : -1;
   };
   constexpr int CPR = RB / 16;  // chunks of a row
   auto kwrite = [&](int i) __attribute__((always_inline)) {

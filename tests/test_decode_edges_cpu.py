@@ -72,3 +72,42 @@ def test_shares_are_even_and_every_number_is_in_its_own(tmp_path):
     for given in (1, 2, 3, 100, 255, 256, 257, 509, 511, 512):
         for start, to in ((1, 3000), ((1 << 24) - 100, (1 << 24) + 100), ((1 << 30) - 100, (1 << 30) + 100), ((1 << 31) - 300, (1 << 31) - 1)):
             assert lib.sweep(start, to, given) == 0, (start, given)
+
+
+def test_looked_up_keys_stay_inside_up_to_the_longest_table(tmp_path):
+    # the lookups that every wave makes in the shares of one sequence, at the
+    # largest table (2^31 - 256 tokens) and at small sizes: the key in 64 bits,
+    # or none past the last tile
+    lib = compiled(tmp_path, r'''
+    int64_t sweep(int len, int columns, int most) {
+      const int U = units_of(len), F = U * columns;
+      const Shares s = make_shares(F, workgroups_of(F, most));
+      int64_t keys = 0;
+      for (int w = 0; w < s.n; ++w)
+        for (int f = share_begin(s, w), end = share_begin(s, w + 1); f < end;) {
+          const int u = f % U, take = end - f < U - u ? end - f : U - u;
+          const int kbeg = u * kUnit, kend = len < kbeg + take * kUnit ? len : kbeg + take * kUnit;
+          for (int wave = 0; wave < 4; ++wave) {
+            const int k1 = kbeg + 32 * wave, last = k1 < kend ? (kend - 1 - k1) / 128 : -1;
+            for (int n = 0; n <= last; n += 32) {
+              if (n == 64 && last > 256) n = (last - 64) / 32 * 32;  // the middle ones are alike
+              for (int lane = 0; lane < 64; ++lane) {
+                const int64_t k = (int64_t)k1 + 128 * (int64_t)(n + (lane >> 1)), kg = k + 16 * (lane & 1);
+                if (looked_up_key(k1, kend, last, n + (lane >> 1), lane & 1) != (k >= kend ? -1 : kg < kend ? kg : k)) return -1;
+                keys += k < kend;
+              }
+            }
+          }
+          f += take;
+        }
+      return keys;
+    }''')
+    lib.sweep.restype = ctypes.c_int64
+    for length in (1, 16, 17, 33, 127, 128, 129, 5003, 100000):
+        for columns in (1, 3):
+            # two lookups a tile
+            assert lib.sweep(length, columns, 256) == 2 * columns * -(-length // 32)
+    for most in (256, 512):
+        for columns in (1, 2, 4, 100):
+            for length in ((1 << 31) - 256, (1 << 31) - 256 - 15, (1 << 31) - 65536):
+                assert lib.sweep(length, columns, most) > 0

@@ -32,3 +32,20 @@ def test_attend_writes_every_head_of_long_sequences(lens, heads, group, head_dim
     q = rand(gen(82), len(lens), heads * group, head_dim, std=1.5, dtype=dtype)
     want, tol = attend_want(pool, q)
     within(attend(pool, q), want, tol, f"{lens} {heads}x{group}")
+
+
+@pytest.mark.parametrize("page,dtype,cache", [(64, "bf16", "bf16"), (16384, "f16", "fp8")])
+def test_attend_over_the_longest_table(page, dtype, cache):
+    # 2^31 - 256 tokens at most, all of whose pages are missing but the first
+    # and the last
+    width = ((1 << 31) - 256) // page
+    small = Pool([2 * page], 4, 64, page, dtype, cache, 83)
+    small.fill(84)
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, -1] = int(small.table[0, 0]), int(small.table[0, 1])
+    q = rand(gen(85), 1, 8, 64, dtype=dtype)
+    want, tol = attend_want(small, q)
+    o = torch.full_like(q, float("nan"), device="cuda")
+    small.cache.attend(q.cuda(), o, table, torch.tensor([(1 << 31) - 1], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    within(o, want, tol, "the longest table")
