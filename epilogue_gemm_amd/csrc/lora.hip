@@ -76,8 +76,11 @@ __device__ __forceinline__ void each_adapter(int id, F&& f) {
 // chunk x of row r at x ^ (r / 2 % 8), which keeps an operand's 16 rows on
 // different banks.  The next stage's loads are in flight while one is
 // multiplied (two or three more of them made it slower, 9.3 to 9.5 us for 16
-// rows, K = 4096 in one kernel).  The waves' parts and the tiles' first stages (`turn`) lie
-// apart, for the memory channels' sake.
+// rows, K = 4096 in one kernel).  The waves' parts and the first stages (`turn`) of
+// the ranges of K, or of the blocks of columns, lie apart, for the memory
+// channels' sake; not those of the tiles, as a row's sums would then depend on
+// where it stands (4096 rows, rank 64: 43.2 us, with them 43.5; each row another
+// of 16 adapters: 289 and 378).
 template <typename T, int RT, int W>
 __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0, int ad, int kbeg, int kend, char* lds,
                                       int wave, int lane, int turn) {
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(256) void shrink(Args a) {
   each_adapter(row_adapter(a, row0 + c), [&](int ad, uint32_t rows) {
     if (number++ % gridDim.z != blockIdx.z) return;
     f32x4 acc[RT] = {};
-    inner<T, RT, 4>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.x);
+    inner<T, RT, 4>(a, acc, row0, ad, kbeg, kend, lds + wave * PER, wave, lane, blockIdx.y);
     __syncthreads();  // every wave has read its operands: their place holds the sums
     float* red = (float*)(lds + wave * PER);
 #pragma unroll

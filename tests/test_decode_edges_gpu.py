@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from epilogue_gemm_amd import binding as gb
-from tests.test_decode_ops_gpu import Pool, attend, attend_want, gen, rand, within
+from tests.test_decode_ops_gpu import Pool, attend, attend_want, gen, lora_case, lora_check, lora_run, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,19 @@ def test_attend_over_the_longest_table(page, dtype, cache):
     small.cache.attend(q.cuda(), o, table, torch.tensor([(1 << 31) - 1], dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     within(o, want, tol, "the longest table")
+
+
+@pytest.mark.parametrize("M,N,K,rank,adapters", [(40, 1000, 1024, 16, 3), (100, 264, 4096, 24, 5), (700, 136, 4096, 64, 4),
+                                                 (1500, 200, 2048, 32, 6)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_lora_of_a_row_in_any_place(M, N, K, rank, adapters, dtype):
+    # one kernel, and two with one range of K and several: the same rows in
+    # another order, so in other tiles and beside other adapters, have the same
+    # bits
+    ids = [(m * 7 + m // 5) % (adapters + 1) - 1 for m in range(M)]
+    x, a, b, ids, s, r = lora_case(M, N, K, rank, adapters, dtype, ids, M + N + K)
+    want = lora_run(x, a, b, ids, s, r, dtype).cpu()
+    lora_check(x, a, b, ids, s, r, want, dtype, "rows in order")
+    for seed in (86, 87):
+        p = torch.randperm(M, generator=gen(seed))
+        assert torch.equal(lora_run(x[p], a, b, ids[p], s, r[p], dtype).cpu(), want[p])
