@@ -282,10 +282,14 @@ __global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
     if (threadIdx.x < 16 * PIECES) {
       const int m = threadIdx.x / PIECES, x = threadIdx.x % PIECES * 8;
       float u[8] = {};
+      // (past the rank stand other rows of A: zero, as an infinity times B's
+      // zeros there would be NaN)
+      if (x < a.rank) {
 #pragma unroll
-      for (int w = 0; w < W; ++w)
+        for (int w = 0; w < W; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] += ((const float*)(lds + w * PER))[m * (RP + 1) + x + e];
+          for (int e = 0; e < 8; ++e) u[e] += ((const float*)(lds + w * PER))[m * (RP + 1) + x + e];
+      }
       u32x4 hi, lo;
       const int ex = split<T, PIECES>(u, hi, lo);
       *(u32x4*)&su[0][m][x] = hi;

@@ -65,3 +65,21 @@ def test_lora_of_a_row_in_any_place(M, N, K, rank, adapters, dtype):
     for seed in (86, 87):
         p = torch.randperm(M, generator=gen(seed))
         assert torch.equal(lora_run(x[p], a, b, ids[p], s, r[p], dtype).cpu(), want[p])
+
+
+@pytest.mark.parametrize("rank,K", [(8, 64), (16, 64), (24, 64), (40, 64), (64, 64), (72, 64), (8, 8200), (24, 8200)])
+def test_lora_infinite_inner_products(rank, K):
+    # U[0] of some rows lies beyond fp32: their C is the infinity of B's sign,
+    # in one kernel and in two, whatever stands behind the rank
+    M, N = 20, 72
+    x, a, b, ids, s, r = lora_case(M, N, K, rank, 2, "bf16", [m % 3 - 1 for m in range(M)], 88)
+    big = (torch.arange(M) % 2 == 0) & (ids >= 0)
+    a[:, 1:, 5] = 0
+    a[:, 0, 5] = 64.0
+    x[:, 5] = 0
+    finite = lora_run(x, a, b, ids, s, r, "bf16").cpu()
+    x[big, 5] = 2.0 ** 127
+    got = lora_run(x, a, b, ids, s, r, "bf16").cpu()
+    assert torch.equal(got[~big], finite[~big]) and bool(finite.isfinite().all())
+    sign = b[ids.clamp(min=0).long()][big][:, :, 0].float().sign()
+    assert torch.equal(got[big].float(), sign * float("inf"))
