@@ -144,17 +144,17 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0,
 
 // Eight values of a row of U, whose other pieces are in the next PIECES - 1
 // lanes, in two 16-bit parts: scaled by 2^-ex, which brings the row's largest
-// value into [1/2, 1), the rounded value and its rounded remainder (U's error
+// finite value into [1/2, 1), the rounded value and its rounded remainder (U's error
 // is the result's).  Returns ex.
 template <typename T, int PIECES>
 __device__ __forceinline__ int split(const float (&u)[8], u32x4& hi, u32x4& lo) {
   float mx = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(u[e]));
+  for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(u[e]) < __builtin_inff() ? fabsf(u[e]) : 0.0f);
 #pragma unroll
   for (int d = 1; d < PIECES; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-  // (an infinite or zero row is left as it is)
-  const int ex = mx > 0.0f && mx < __builtin_inff() ? max(__builtin_amdgcn_frexp_expf(mx), -120) : 0;
+  // (a row of zeros is left as it is)
+  const int ex = mx > 0.0f ? max(__builtin_amdgcn_frexp_expf(mx), -120) : 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float v0 = __builtin_amdgcn_ldexpf(u[2 * e], -ex), v1 = __builtin_amdgcn_ldexpf(u[2 * e + 1], -ex);

@@ -83,3 +83,15 @@ def test_lora_infinite_inner_products(rank, K):
     assert torch.equal(got[~big], finite[~big]) and bool(finite.isfinite().all())
     sign = b[ids.clamp(min=0).long()][big][:, :, 0].float().sign()
     assert torch.equal(got[big].float(), sign * float("inf"))
+
+
+@pytest.mark.parametrize("M,K", [(6, 64), (6, 8200)])
+def test_lora_finite_inner_products_beside_an_infinite_one(M, K):
+    # U = (infinity, 2^17, ...) in F16: the second, beyond the largest F16 but
+    # finite, takes nothing from the first
+    x, a, b, ids, _, r = lora_case(M, 40, K, 8, 1, "f16", [0] * M, 89)
+    a[0, :2], x[:, 7:9] = 0, 0
+    a[0, 0, 7], a[0, 1, 8], b[0, :, 0], b[0, :, 1] = float("inf"), 512.0, 1.0, -1.0
+    a[0, 1:, 7] = 0
+    x[:, 7], x[:, 8] = 1.0, 256.0
+    assert bool((lora_run(x, a, b, ids, None, r, "f16") == float("inf")).all())
