@@ -3,9 +3,9 @@
 Every .hip/.cpp file under csrc/ is compiled by hipcc for gfx950 only, in
 parallel, then linked into epilogue_gemm_amd/libgemm_epi.so; torch_calls.cpp,
 the host-only module that checks torch tensors for binding.py, is compiled by
-g++ into _calls.so against the Python and torch headers.  build() recompiles
-everything by default (it is the "does it build" check);
-build(incremental=True) (``python -m epilogue_gemm_amd.build --incremental``)
+g++ into _calls.so against the Python and torch headers, where torch is
+installed.  build() recompiles everything by default (it is the "does it
+build" check); build(incremental=True) (``python -m epilogue_gemm_amd.build --incremental``)
 recompiles only the sources whose object is older than the source or any
 header it includes (from the compiler's dependency files).
 """
@@ -80,10 +80,14 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_calls() -> None:
+def _build_calls() -> bool:
     """_calls.so; it finds the library beside itself, and torch's libraries
-    loaded (binding.py imports torch first)."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    loaded (binding.py imports torch first).  Not built, and False, where
+    torch is not installed: the C library does not need it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return False
+    torch = spec.submodule_search_locations[0]
     tmp = CALLS + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", "-isystem", os.path.join(torch, "include"),
            "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp, "-L", HERE, "-l:" + os.path.basename(LIB),
@@ -92,6 +96,7 @@ def _build_calls() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    return True
 
 
 def build(jobs: int | None = None, verbose: bool = False, incremental: bool = False) -> str:
@@ -110,9 +115,9 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_calls()
+    calls = CALLS if _build_calls() else f"not {CALLS} (the tensor calls): torch is not installed"
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources, {CALLS}")
+        print(f"built {LIB} from {len(srcs)} sources, {calls}")
     return LIB
 
 

@@ -111,3 +111,18 @@ def test_looked_up_keys_stay_inside_up_to_the_longest_table(tmp_path):
         for columns in (1, 2, 4, 100):
             for length in ((1 << 31) - 256, (1 << 31) - 256 - 15, (1 << 31) - 65536):
                 assert lib.sweep(length, columns, most) > 0
+
+
+def test_the_library_builds_without_torch(monkeypatch, tmp_path, capsys):
+    # build() up to its end on a machine without torch: the C library linked,
+    # the tensor calls left out
+    from epilogue_gemm_amd import build as b
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(b, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(b, "sources", lambda: [os.path.join(b.CSRC, "tuning.cpp")])
+    found = b.importlib.util.find_spec
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name, *a: None if name == "torch" else found(name, *a))
+    b.build(verbose=True)
+    assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
+    assert "torch is not installed" in capsys.readouterr().out
