@@ -479,7 +479,8 @@ constexpr int64_t kLim = (int64_t)1 << 31;
 // The sizes a call would run (M = 0 included).
 gemm_epi_status check_sizes(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters) {
   if (M < 0 || N <= 0 || K <= 0 || rank <= 0 || adapters <= 0) return GEMM_EPI_ERR_INVALID_ARG;
-  if (rank > 128 || rank % 8 != 0 || K % 8 != 0 || M >= kLim / 8 || K >= kLim / 8 || adapters > 65535 ||
+  // (a tile of 16 rows a workgroup of 256: a grid holds below 2^32 threads)
+  if (rank > 128 || rank % 8 != 0 || K % 8 != 0 || M > kLim / 8 - 16 || K >= kLim / 8 || adapters > 65535 ||
       N > (int64_t)65535 * 256)
     return GEMM_EPI_ERR_UNSUPPORTED;
   return GEMM_EPI_OK;

@@ -762,7 +762,8 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
   if (!formats_fit(cache, dtype) || tokens < 0 || ldk < row || ldv < row || ((uintptr_t)starts & 3u) ||
       (!starts && tokens != table->batch))
     return GEMM_EPI_ERR_INVALID_ARG;
-  if (tokens >= (int64_t)1 << 26 || ldk % 8 != 0 || ldv % 8 != 0) return GEMM_EPI_ERR_UNSUPPORTED;
+  // (four tokens a workgroup of 256: a grid holds below 2^32 threads)
+  if (tokens > ((int64_t)1 << 26) - 4 || ldk % 8 != 0 || ldv % 8 != 0) return GEMM_EPI_ERR_UNSUPPORTED;
   if (tokens == 0 || table->batch == 0) return GEMM_EPI_OK;
   if (!K || !V) return GEMM_EPI_ERR_INVALID_ARG;
   if (((uintptr_t)K | (uintptr_t)V) & 15u) return GEMM_EPI_ERR_UNSUPPORTED;

@@ -81,8 +81,8 @@ gemm_epi_status gemm_epi_rmsnorm(const void* X, int64_t ldx, const void* R, int6
  * or adapters <= 0, a leading dimension below its row, dtype not F16/BF16,
  * workspace missing or too small, a pointer off its element's alignment),
  * UNSUPPORTED (rank above 128 or not a multiple of 8, K not a multiple of 8,
- * ldx not a multiple of 8, X, A, B or workspace not 16-byte aligned, M or K
- * >= 2^28, N above 65535 * 256, more than 65535 adapters),
+ * ldx not a multiple of 8, X, A, B or workspace not 16-byte aligned, M above
+ * 2^28 - 16, K >= 2^28, N above 65535 * 256, more than 65535 adapters),
  * HIP. */
 gemm_epi_status gemm_epi_lora(const void* X, int64_t ldx, const void* A, const void* B, const float* scale,
                               const int32_t* ids, const void* R, int64_t ldr, void* C, int64_t ldc, int64_t M,
@@ -156,7 +156,7 @@ typedef struct gemm_epi_page_table {
  * UNSUPPORTED (head_dim not 64 or 128, page_size not a multiple of 16 or
  * above 65536, more than 1024 heads, num_pages * page_size >= 2^31, width *
  * page_size above 2^31 - 256, batch times the 128-token units of width *
- * page_size >= 2^31, tokens >= 2^26, batch > 65535; a pointer of the cache, K
+ * page_size >= 2^31, tokens above 2^26 - 4, batch > 65535; a pointer of the cache, K
  * or V that is not 16-byte aligned, ldk or ldv not a multiple of 8), HIP. */
 gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const gemm_epi_page_table* table,
                                       const void* K, int64_t ldk, const void* V, int64_t ldv, const int32_t* starts,

@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+from epilogue_gemm_amd import binding as gb
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -126,3 +128,16 @@ def test_the_library_builds_without_torch(monkeypatch, tmp_path, capsys):
     b.build(verbose=True)
     assert os.path.exists(b.LIB) and not os.path.exists(b.CALLS)
     assert "torch is not installed" in capsys.readouterr().out
+
+
+def test_sizes_that_no_grid_holds_are_refused():
+    # 2^24 workgroups of 256 would be 2^32 threads
+    OK, INVALID, UNSUPPORTED, P = 0, 1, 2, 0x10000
+    cache = gb.paged_cache_struct(P, P, None, None, 9, 16, 2, 64, "bf16")
+    table = gb.page_table_struct(P, 4, 4, P, 0)  # (no sequences: nothing is launched)
+    for tokens, want in (((1 << 26) - 4, OK), ((1 << 26) - 3, UNSUPPORTED), ((1 << 26) - 1, UNSUPPORTED)):
+        assert gb.gemm_epi_cache_append(cache, table, P, 128, P, 128, P, tokens, "bf16", None) == want
+    for M, want in (((1 << 28) - 16, INVALID), ((1 << 28) - 15, UNSUPPORTED), ((1 << 28) - 1, UNSUPPORTED)):
+        # (no ids: refused before anything is launched)
+        assert gb.gemm_epi_lora(P, 64, P, P, None, None, None, 0, P, 64, M, 64, 64, 8, 2, "f16", P, 1 << 60, None) == want
+        assert (gb.gemm_epi_lora_workspace_size(M, 64, 64, 8, 2) > 0) == (want == INVALID)
