@@ -71,18 +71,24 @@ GE_HD int units_of(int len) { return len / kUnit + (len % kUnit != 0); }
 GE_HD int workgroups_of(int F, int most) { return most > 256 && F <= 2 * most ? 256 : most; }
 struct Shares {
   int n, base, more;  // shares, numbers in each, and how many have one more
+  uint32_t inv;       // 2^32 / n, rounded up (n = 1: 0, as `more` then is)
+  float ratio;        // n / F
 };
 GE_HD Shares make_shares(int F, int workgroups) {
   const int n = F < workgroups ? F : workgroups;
-  return n == 0 ? Shares{0, 0, 0} : Shares{n, (int)((uint32_t)F / (uint32_t)n), (int)((uint32_t)F % (uint32_t)n)};
+  if (n == 0) return Shares{0, 0, 0, 0, 0.0f};
+  return Shares{n, (int)((uint32_t)F / (uint32_t)n), (int)((uint32_t)F % (uint32_t)n), 0xffffffffu / (uint32_t)n + 1,
+                (float)n / (float)F};
 }
-// floor(w F / n), with F = n base + more (n below 2^16).
-GE_HD int share_begin(Shares s, int w) { return w * s.base + (int)((uint32_t)(w * s.more) / (uint32_t)s.n); }
+// floor(w F / n), with F = n base + more: w more is below 2^18 (n is 512 at
+// most), so that inv's error adds less than 2^-14, and so less than 1 / n.
+GE_HD int share_begin(Shares s, int w) {
+  return w * s.base + (int)(((uint64_t)(uint32_t)(w * s.more) * s.inv) >> 32);
+}
 // The share that has number f < F: f n / F in fp32 is within one of it, as
 // every rounding is at most 2^-24 of a number of at most n.
 GE_HD int share_of(Shares s, int f) {
-  const int at = (int)((float)f * ((float)s.n / ((float)s.base * (float)s.n + (float)s.more)));
-  const int w = at < s.n ? at : s.n - 1;
+  const int at = (int)((float)f * s.ratio), w = at < s.n ? at : s.n - 1;
   return w + (w + 1 < s.n && share_begin(s, w + 1) <= f) - (share_begin(s, w) > f);
 }
 

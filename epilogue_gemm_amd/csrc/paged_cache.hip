@@ -151,6 +151,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 constexpr int kWorkgroups = 512;
 inline int workgroups_for(int row_bytes) { return row_bytes >= 128 ? 256 : kWorkgroups; }
 static_assert(kWorkgroups * 4 == GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES, "a counter each");
+static_assert(kWorkgroups <= 512, "share_begin");
 
 struct DecodeArgs {
   const char *k, *v;
