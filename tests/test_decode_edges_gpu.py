@@ -95,3 +95,19 @@ def test_lora_finite_inner_products_beside_an_infinite_one(M, K):
     a[0, 1:, 7] = 0
     x[:, 7], x[:, 8] = 1.0, 256.0
     assert bool((lora_run(x, a, b, ids, None, r, "f16") == float("inf")).all())
+
+
+@pytest.mark.parametrize("head_dim,cache", [(64, "f16"), (128, "f16"), (64, "fp8"), (128, "fp8")])
+def test_attend_small_weights_beside_large_ones(head_dim, cache):
+    # every 16th key has e^11 to e^13 times the weight of each other, but zeros
+    # for a value: the others' weights in F16 would be multiples of 2^-24, a
+    # hundredth of them
+    n = 3000
+    pool = Pool([n], 1, head_dim, 64, "f16", cache, 90)
+    k, v = torch.zeros(n, 1, head_dim, dtype=torch.float16), torch.full((n, 1, head_dim), 16.0, dtype=torch.float16)
+    k[::16, 0, 0], v[::16] = 12, 0
+    pool.held = [(pool.put(pool.k, pool.ks, 0, k), pool.put(pool.v, pool.vs, 0, v))]
+    q = torch.zeros(1, 16, head_dim, dtype=torch.float16)
+    q[0, :, 0] = (7.5 + torch.arange(16) / 16) * (head_dim / 64) ** 0.5
+    want, tol = attend_want(pool, q)
+    within(attend(pool, q), want, tol, "small weights")
