@@ -308,12 +308,12 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   // 8-bit rows of f16 values up to 65504 have codes times scales up to 65536,
   // which f16 does not hold: both products take f16's values halved
   constexpr float kHalf = FP8 && __is_same(T, f16) ? 0.5f : 1.0f;
-  // f16 has fewer bits below 2^-14, and there are the weights of most keys
-  // beside one that stands out (2^-17 was off by up to 0.5 %): they are taken
-  // times 2^12.  The two parts then lose 2^-22 of a weight of 2^-15 of the
-  // largest and more, and 2^-37 of the largest of smaller ones.  The sums carry
-  // the factor too, so that it leaves no trace.
-  constexpr float kWeightLog2 = __is_same(T, f16) ? 12.0f : 0.0f;
+  // The weights are taken relative to 2^-7 of the largest in f16, which has
+  // fewer bits below 2^-14: there are the weights of most keys beside one that
+  // stands out (one of 2^-17 was off by up to 0.5 %).  The two parts then lose
+  // 2^-22 of a weight of 2^-10 of the largest and more, and 2^-32 of the largest
+  // of smaller ones; no weight is above 2^8, however maximum - 7 is rounded.
+  constexpr float kAbove = __is_same(T, f16) ? 7.0f : 0.0f;
   __shared__ float sm[4][16], sl[4][16];
   __shared__ __attribute__((aligned(16))) float so[4][16][D + 4];
   __shared__ int last_arrived;
@@ -476,11 +476,13 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
         for (int e = 0; e < 4; ++e)
           if (4 * h + e >= t.valid[g]) s[g][e] = kNegInf;
     }
-    // running maximum of the query head over all four quarters; the sums are
-    // rescaled only when some head's maximum moves
+    // the reference of the weights: the running maximum of the query head over
+    // all four quarters, less kAbove; the sums are rescaled only when some
+    // head's moves
     float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
     mx = wave::over_rows<wave::Max>(mx);
+    if constexpr (kAbove != 0.0f) mx -= kAbove;
     if (__builtin_amdgcn_ballot_w64(mx > m)) {
       const float mn = fmaxf(m, mx);
       const float alpha = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.0f : mn));
@@ -490,16 +492,12 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
     }
     const float ref = m == kNegInf ? 0.0f : m;
-    auto weight = [&](float x) __attribute__((always_inline)) {
-      x -= ref;
-      if constexpr (kWeightLog2 != 0.0f) x += kWeightLog2;
-      return __builtin_amdgcn_exp2f(x);
-    };
     // probabilities, in two parts
     u32x4 ph, pl;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float p0 = weight(s[w >> 1][2 * (w & 1)]), p1 = weight(s[w >> 1][2 * (w & 1) + 1]);
+      const float p0 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1)] - ref);
+      const float p1 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1) + 1] - ref);
       l += p0 + p1;
       const T t0 = from_f32<T>(p0), t1 = from_f32<T>(p1);
       ph[w] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
