@@ -32,6 +32,8 @@
 
 #include "../../include/gemm_epi_decode.h"
 
+#include <type_traits>
+
 namespace ge {
 namespace paged {
 
@@ -295,8 +297,7 @@ struct Tile {
   typedef uint32_t vwords __attribute__((ext_vector_type(VW == 1 ? 2 : VW)));  // (one word: in .x)
   u32x4 k[2][KL];
   vwords v[8];
-  float ks[2];
-  f32x4 vs[2];
+  f32x4 ks[2], vs[2];
   int valid[2];
 };
 
@@ -305,15 +306,18 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   using Tl = Tile<FP8, D>;
   constexpr int VEC = Tl::VEC, EB = Tl::EB, KL = Tl::KL, VW = Tl::VW, RB = Tl::RB;
   constexpr int KS = D / 32;  // 32-deep steps of a score
-  // 8-bit rows of f16 values up to 65504 have codes times scales up to 65536,
-  // which f16 does not hold: both products take f16's values halved
-  constexpr float kHalf = FP8 && __is_same(T, f16) ? 0.5f : 1.0f;
+  // f16 does not hold every code times its scale (65504 is held as 256 times
+  // 2^8, and small rows lie below 2^-14).  Beside f16 queries K's codes enter
+  // their product as they are and the scores take the scales; the second product
+  // of an 8-bit cache is bf16's, which has room for all of V's.
+  constexpr bool kCodes = FP8 && __is_same(T, f16);
+  typedef std::conditional_t<FP8, bf16, T> TV;
   // The weights are taken relative to 2^-7 of the largest in f16, which has
   // fewer bits below 2^-14: there are the weights of most keys beside one that
   // stands out (one of 2^-17 was off by up to 0.5 %).  The two parts then lose
   // 2^-22 of a weight of 2^-10 of the largest and more, and 2^-32 of the largest
   // of smaller ones; no weight is above 2^8, however maximum - 7 is rounded.
-  constexpr float kAbove = __is_same(T, f16) ? 7.0f : 0.0f;
+  constexpr float kAbove = __is_same(TV, f16) ? 7.0f : 0.0f;
   __shared__ float sm[4][16], sl[4][16];
   __shared__ __attribute__((aligned(16))) float so[4][16][D + 4];
   __shared__ int last_arrived;
@@ -430,7 +434,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
         else t.v[4 * g + u] = __builtin_nontemporal_load((const typename Tl::vwords*)r);
       }
       if constexpr (FP8) {
-        t.ks[g] = a.ks[row + c];
+        if constexpr (kCodes) t.ks[g] = *(const f32x4*)(a.ks + row + 4 * h);
+        else t.ks[g].x = a.ks[row + c];
         t.vs[g] = *(const f32x4*)(a.vs + row + 4 * h);
       }
     }
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
           const u32x4 x = kf[i];
-          const float f = t.ks[g] * kHalf;
+          const float f = kCodes ? 1.0f : t.ks[g].x;
           const u32x4 lo = {widen2<T, false>(x[0], f), widen2<T, true>(x[0], f), widen2<T, false>(x[1], f),
                             widen2<T, true>(x[1], f)};
           const u32x4 hi = {widen2<T, false>(x[2], f), widen2<T, true>(x[2], f), widen2<T, false>(x[3], f),
@@ -467,7 +472,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) s[g] = mfma16<T>(kf[i], qf[i], s[g]);
       }
-      s[g] *= a.scale_log2 * (1.0f / kHalf);
+      if constexpr (kCodes) s[g] *= t.ks[g] * a.scale_log2;
+      else s[g] *= a.scale_log2;
     }
     if (!whole) {
 #pragma unroll
@@ -499,20 +505,20 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       const float p0 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1)] - ref);
       const float p1 = __builtin_amdgcn_exp2f(s[w >> 1][2 * (w & 1) + 1] - ref);
       l += p0 + p1;
-      const T t0 = from_f32<T>(p0), t1 = from_f32<T>(p1);
+      const TV t0 = from_f32<TV>(p0), t1 = from_f32<TV>(p1);
       ph[w] = (uint32_t)bits16(t0) | (uint32_t)bits16(t1) << 16;
-      pl[w] = pack2_out<T>(p0 - to_f32(t0), p1 - to_f32(t1));
+      pl[w] = pack2_out<TV>(p0 - to_f32(t0), p1 - to_f32(t1));
     }
     // V: this lane's eight keys, 16-bit
     uint32_t vr[8][VEC / 2];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if constexpr (FP8) {
-        const float f = t.vs[u >> 2][u & 3] * kHalf;
+        const float f = t.vs[u >> 2][u & 3];
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          vr[u][2 * w] = widen2<T, false>(t.v[u][w], f);
-          vr[u][2 * w + 1] = widen2<T, true>(t.v[u][w], f);
+          vr[u][2 * w] = widen2<TV, false>(t.v[u][w], f);
+          vr[u][2 * w + 1] = widen2<TV, true>(t.v[u][w], f);
         }
       } else {
 #pragma unroll
@@ -535,8 +541,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
 #pragma unroll
       for (int w = 0; w < 4; ++w)
         vf[w] = __builtin_amdgcn_perm(vr[2 * w + 1][j >> 1], vr[2 * w][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
-      acc[j] = mfma16<T>(vf, ph, acc[j]);
-      acc[j] = mfma16<T>(vf, pl, acc[j]);
+      acc[j] = mfma16<TV>(vf, ph, acc[j]);
+      acc[j] = mfma16<TV>(vf, pl, acc[j]);
     }
   };
   // The next tile's loads are in flight while one is multiplied.
@@ -578,8 +584,6 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       o0 += x * so[i][qh][d];
       o1 += x * so[i][qh][d + 1];
     }
-    o0 *= 1.0f / kHalf;
-    o1 *= 1.0f / kHalf;
     if (take == units) {
       const float inv = lj == 0.0f ? 0.0f : 1.0f / lj;
       *(uint32_t*)((T*)a.O + seq * a.ldo + (int64_t)(head * a.group + first + qh) * D + d) = pack2_out<T>(o0 * inv, o1 * inv);

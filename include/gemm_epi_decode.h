@@ -179,12 +179,11 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
  * in the scales there is read into no result, NaN included.
  * Scores, softmax and accumulation in fp32; the probabilities enter the
  * second product as two 16-bit parts (their rounded value and its rounded
- * remainder, in F16 of 2^7 times their ratio to the largest); an FP8_E4M3
- * cache's values enter the products in the format of Q: exactly, but in F16
- * those below 2^-13 to a multiple of 2^-23 and those of a scale above 2^8
- * perhaps as infinities; O is rounded once.  The keys
- * are split over workgroups by the lengths found on the device and joined in
- * a fixed order: the same inputs give the same bits.
+ * remainder), in F16 of 2^7 times their ratio to the largest, in BF16 and for
+ * an FP8_E4M3 cache in BF16; such a cache's values enter both products exactly
+ * (from 2^128 on as infinities); O is rounded once.  The keys are split over
+ * workgroups by the lengths found on the device and joined in a fixed order:
+ * the same inputs give the same bits.
  * workspace: gemm_epi_attention_decode_workspace_size bytes, 16-byte aligned.
  * Its first GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES hold counters: zero-filled
  * once before its first use, and left zero by every run that completes; the

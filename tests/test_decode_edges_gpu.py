@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from epilogue_gemm_amd import binding as gb
-from tests.test_decode_ops_gpu import Pool, attend, attend_want, gen, lora_case, lora_check, lora_run, rand, within
+from tests.test_decode_ops_gpu import Pool, attend, attend_want, gen, lora_case, lora_check, lora_run, pow2_quantise, rand, within
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,45 @@ def test_attend_small_weights_beside_large_ones(head_dim, cache):
     q[0, :, 0] = (7.5 + torch.arange(16) / 16) * (head_dim / 64) ** 0.5
     want, tol = attend_want(pool, q)
     within(attend(pool, q), want, tol, "small weights")
+
+
+def test_attend_smallest_f16_values_in_8_bits():
+    # rows of 2^-13 and, beside it, 9 2^-24, which E4M3 holds exactly at the
+    # rows' scale 2^-21: exact in both products, as a multiple of F16's least
+    # step 2^-24
+    n, D = 500, 64
+    pool = Pool([n], 1, D, 16, "f16", "fp8", 91)
+    small, odd = 9 * 2.0 ** -24, torch.arange(n) % 2 == 1
+    k, v = torch.zeros(n, 1, D, dtype=torch.float16), torch.full((n, 1, D), small, dtype=torch.float16)
+    k[:, 0, 0], v[:, 0, 0] = 2.0 ** -13, 2.0 ** -13
+    k[odd, 0, 1:] = small
+    v[odd, 0, 1:8] = 2.0 ** -13
+    pool.held = [(pool.put(pool.k, pool.ks, 0, k), pool.put(pool.v, pool.vs, 0, v))]
+    assert torch.equal(pool.held[0][0], k.double()) and torch.equal(pool.held[0][1], v.double())
+    q = torch.zeros(1, 4, D, dtype=torch.float16)
+    q[0, 1:, 1:] = torch.tensor([2.0 ** 14, 2.0 ** 15, 65504.0]).half()[:, None]
+    want, tol = attend_want(pool, q)
+    within(attend(pool, q), want, tol, "smallest values")
+
+
+def test_attend_scales_beyond_those_of_f16_rows():
+    # a cache filled by another's hand: K's scales of any size, V's up to 2^14
+    n, D = 300, 64
+    pool = Pool([n], 2, D, 32, "f16", "fp8", 92)
+    pool.fill(93)
+    kv = []
+    for values, cache, scale, powers in zip(pool.held[0], (pool.k, pool.v), (pool.ks, pool.vs), ([-90, -20, 0, 16, 20], [-20, 4, 8, 11, 14])):
+        q, s = pow2_quantise(values)
+        s = torch.exp2(torch.tensor(powers)[torch.randint(0, 5, s.shape, generator=gen(94))].double())
+        q = q.clamp(-3, 3)  # (so that O is within F16)
+        q = q.float().to(torch.float8_e4m3fn)
+        pos = torch.arange(n)
+        page, slot = pool.table[0].long()[pos // 32].cuda(), (pos % 32).cuda()
+        cache.view(torch.uint8)[page, :, slot] = q.cuda().view(torch.uint8)
+        scale[page, :, slot] = s.float().cuda()
+        kv.append(q.float().double() * s[..., None])
+    pool.held = [tuple(kv)]
+    q = torch.randn(1, 4, D, generator=gen(95)) * 2.0 ** -24 * torch.tensor([1.0, 2.0, 4.0, 8.0])[:, None]
+    q = q.half()
+    want, tol = attend_want(pool, q)
+    within(attend(pool, q), want, tol, "large scales")
