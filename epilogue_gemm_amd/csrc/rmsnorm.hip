@@ -251,7 +251,7 @@ extern "C" gemm_epi_status gemm_epi_rmsnorm(const void* X, int64_t ldx, const vo
   if (dtype != GEMM_EPI_F16 && dtype != GEMM_EPI_BF16) return GEMM_EPI_ERR_INVALID_ARG;
   const bool fp8 = out_dtype == GEMM_EPI_FP8_E4M3;
   if (!fp8 && out_dtype != dtype) return GEMM_EPI_ERR_INVALID_ARG;
-  if (rows < 0 || cols <= 0 || !(eps >= 0.0f) || eps > 3.0e38f) return GEMM_EPI_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || !(eps >= 0.0f) || eps == __builtin_inff()) return GEMM_EPI_ERR_INVALID_ARG;
   if (ldx < cols || ldy < cols || (R && ldr < cols) || (H && ldh < cols)) return GEMM_EPI_ERR_INVALID_ARG;
   if (!X || !W || !Y || fp8 != (y_scale != nullptr)) return GEMM_EPI_ERR_INVALID_ARG;
   const int64_t lim = (int64_t)1 << 31;

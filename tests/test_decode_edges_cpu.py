@@ -141,3 +141,9 @@ def test_sizes_that_no_grid_holds_are_refused():
         # (no ids: refused before anything is launched)
         assert gb.gemm_epi_lora(P, 64, P, P, None, None, None, 0, P, 64, M, 64, 64, 8, 2, "f16", P, 1 << 60, None) == want
         assert (gb.gemm_epi_lora_workspace_size(M, 64, 64, 8, 2) > 0) == (want == INVALID)
+
+
+def test_rmsnorm_takes_any_finite_eps():
+    for eps, want in ((0.0, 0), (3.4e38, 0), (3.5e38, 1), (float("inf"), 1), (float("nan"), 1), (-1e-45, 1)):
+        # (no rows: nothing is launched; 3.5e38 is an infinity in fp32)
+        assert gb.gemm_epi_rmsnorm(0x10000, 64, None, 0, 0x10000, None, 0, 0x10000, 64, None, 0, 64, eps, "bf16", "bf16", None) == want
