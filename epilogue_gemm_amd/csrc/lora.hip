@@ -403,9 +403,13 @@ __global__ __launch_bounds__(ONE ? 512 : 256) void expand(Args a) {
 
 // Ranges of K, by the sizes alone.  Up to 1024 rows eight of 512 or more,
 // which give the chip work (K = N = 4096, two kernels: 16 rows 8.7 us, one
-// range 11.1; 512 rows, rank 64, 15.3 against 20.2); more rows one, as partial sums then cost
-// what the ranges gain (4096 rows, rank 64: 43.4 us, two 44.8, four 42.6; rank
-// 16 29.0, 29.0, 30.4).
+// range 11.1; 512 rows, rank 64, 15.3 against 20.2).  More rows one, for the
+// batches in which each row has another adapter, whose A then passes through a
+// CU once a range and tile (2048 rows, rank 64: 139 us, two ranges 195; 4096
+// rows 289 and 335).  Long runs of an adapter would rather have two up to 2048
+// rows (1100 rows, rank 64: 23.9 and 20.7; 2000 rows 27.7 and 26.8) and gain
+// nothing above (4096 rows, rank 64: 43.2, two 44.7, four 42.7; rank 16 29.2,
+// 29.3, 30.6).
 struct Cut {
   int tiles, ksplit, kper;
 };

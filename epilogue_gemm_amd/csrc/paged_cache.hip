@@ -32,8 +32,6 @@
 
 #include "../../include/gemm_epi_decode.h"
 
-#include <type_traits>
-
 namespace ge {
 namespace paged {
 
@@ -498,7 +496,9 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       for (int j = 0; j < VEC; ++j) acc[j] *= alpha;
     }
     const float ref = m == kNegInf ? 0.0f : m;
-    // probabilities, in two parts
+    // probabilities, in two parts (fp32 products have a sixteenth of the rate;
+    // one 16-bit part alone would be off by as much as the output's rounding:
+    // two lose 2^-16 of each weight in bf16, a 256th of that rounding)
     u32x4 ph, pl;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
