@@ -7,7 +7,7 @@
 // that the chip holds at once (paged.hpp), and the pieces of a sequence that
 // the split cuts joined by the workgroup that finishes last, or, where they
 // are many, by a second kernel.  Bound by the cache's bytes (32 x 8192 bf16
-// of mixed lengths, 8 heads of 128: 89 us, 5.9 TB/s), for few keys by the
+// of mixed lengths, 8 heads of 128: 88 us, 6.0 TB/s), for few keys by the
 // chain of lookups, loads and the join (1 x 1000: 8.3 us, 3 of them the join).
 //
 // For each piece -- some keys of one sequence, one key head and up to 16 of
