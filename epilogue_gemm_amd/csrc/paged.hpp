@@ -92,6 +92,15 @@ GE_HD int share_of(Shares s, int f) {
   return w + (w + 1 < s.n && share_begin(s, w + 1) <= f) - (share_begin(s, w) > f);
 }
 
+// The share of a workgroup < n.  Workgroups go to the 8 XCDs in turn: consecutive
+// shares go to one XCD, so that all have as many of the larger ones (share w to
+// workgroup w, these can all fall on one: 48 x 700, 8 heads of 128, bf16, 24.2 and
+// 22.1 us; 64 x 1000 E4M3 27.8 and 26.4).  Other n than multiples of 8 are those of
+// few units, one a share.
+GE_HD int share_at(Shares s, int workgroup) {
+  return s.n % 8 != 0 ? workgroup : workgroup % 8 * (s.n / 8) + workgroup / 8;
+}
+
 // A wave's tiles of 32 keys are 128 keys apart, from key k1 on; tile `last` is its
 // last one before kend.  The key whose page is looked up for one of the two
 // groups of 16 of a tile: past the sequence's end the tile's first, past the last

@@ -205,7 +205,7 @@ __device__ __forceinline__ int len_of(const Units& un, const int32_t* lens, int 
                      : __builtin_amdgcn_readfirstlane(seq_len(lens[seq], cap));
 }
 
-// Piece `which` of workgroup w: 0 of a sequence that began in an earlier
+// Piece `which` of share w: 0 of a sequence that began in an earlier
 // workgroup's share, 1 of one that begins in this one's and ends later.
 template <int D>
 __device__ __forceinline__ float* part_of(const DecodeArgs& a, int w, int which) {
@@ -329,11 +329,10 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
   const int cap = a.width * a.page_size;
 
   const int columns = a.heads * a.qtiles;
-  const int w = blockIdx.x;
   const Units un = count_units(a.lens, a.batch, cap, lane);
   // an empty sequence has no units: its zeros are written here
   if (un.empty)
-    for (int i = w; i < a.batch * columns; i += gridDim.x) {
+    for (int i = blockIdx.x; i < a.batch * columns; i += gridDim.x) {
       const int seq = i / columns, col = i % columns;
       if (seq_len(a.lens[seq], cap) != 0) continue;
       const int qh = (col % a.qtiles) * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * VEC;
@@ -343,7 +342,8 @@ __global__ __launch_bounds__(256, 2) void decode_kernel(DecodeArgs a) {
       for (int j = 0; j < VEC; j += 2) *(uint32_t*)(op + j) = 0u;
     }
   const Shares sh = make_shares(un.total * columns, workgroups_of(un.total * columns, gridDim.x));
-  if (w >= sh.n) return;
+  if ((int)blockIdx.x >= sh.n) return;
+  const int w = share_at(sh, blockIdx.x);
   int f = share_begin(sh, w);
   const int fend = share_begin(sh, w + 1);
   int column = (int)((uint32_t)f / (uint32_t)un.total), u = f - column * un.total;  // unit u of this column is next

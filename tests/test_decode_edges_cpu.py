@@ -76,6 +76,23 @@ def test_shares_are_even_and_every_number_is_in_its_own(tmp_path):
             assert lib.sweep(start, to, given) == 0, (start, given)
 
 
+def test_every_share_is_one_workgroups(tmp_path):
+    # and the larger shares are spread over the workgroups that share an XCD
+    lib = compiled(tmp_path, r"""
+    int c_shares(int F, int given) { return make_shares(F, given).n; }
+    int c_share_at(int F, int given, int workgroup) { return share_at(make_shares(F, given), workgroup); }
+    int c_size(int F, int given, int w) { const Shares s = make_shares(F, given); return share_begin(s, w + 1) - share_begin(s, w); }
+    """)
+    for given in (1, 7, 8, 100, 256, 512):
+        for F in (1, 5, 8, 250, 256, 257, 300, 528, 1000, 4100, 100003):
+            n = lib.c_shares(F, given)
+            at = [lib.c_share_at(F, given, b) for b in range(n)]
+            assert sorted(at) == list(range(n))
+            if n % 8 == 0:
+                units = [sum(lib.c_size(F, given, w) for w in at[x::8]) for x in range(8)]
+                assert max(units) - min(units) <= 1, (F, given, units)
+
+
 def test_looked_up_keys_stay_inside_up_to_the_longest_table(tmp_path):
     # the lookups that every wave makes in the shares of one sequence, at the
     # largest table (2^31 - 256 tokens) and at small sizes: the key in 64 bits,
