@@ -144,8 +144,10 @@ __device__ __forceinline__ void inner(const Args& a, f32x4 (&acc)[RT], int row0,
 
 // Eight values of a row of U, whose other pieces are in the next PIECES - 1
 // lanes, in two 16-bit parts: scaled by 2^-ex, which brings the row's largest
-// finite value into [1/2, 1), the rounded value and its rounded remainder (U's error
-// is the result's).  Returns ex.
+// finite value into [1/2, 1), in f16, whose small values have fewer bits, into
+// [2^14, 2^15), the rounded value and its rounded remainder (U's error is the
+// result's: 2^-16 of a value in bf16, 2^-22 in f16 down to 2^-18 of the largest
+// and 2^-39 of that below).  Returns ex.
 template <typename T, int PIECES>
 __device__ __forceinline__ int split(const float (&u)[8], u32x4& hi, u32x4& lo) {
   float mx = 0.0f;
@@ -154,7 +156,7 @@ __device__ __forceinline__ int split(const float (&u)[8], u32x4& hi, u32x4& lo) 
 #pragma unroll
   for (int d = 1; d < PIECES; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
   // (a row of zeros is left as it is)
-  const int ex = mx > 0.0f ? max(__builtin_amdgcn_frexp_expf(mx), -120) : 0;
+  const int ex = mx > 0.0f ? max(__builtin_amdgcn_frexp_expf(mx), -120) - (__is_same(T, f16) ? 15 : 0) : 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float v0 = __builtin_amdgcn_ldexpf(u[2 * e], -ex), v1 = __builtin_amdgcn_ldexpf(u[2 * e + 1], -ex);

@@ -97,6 +97,19 @@ def test_lora_finite_inner_products_beside_an_infinite_one(M, K):
     assert bool((lora_run(x, a, b, ids, None, r, "f16") == float("inf")).all())
 
 
+@pytest.mark.parametrize("M,K", [(20, 64), (20, 8200)])
+def test_lora_small_inner_products_beside_a_large_one(M, K):
+    # U = (4096, some 2^-8, 0, ...) in F16, of which only the second has a
+    # column of B, of ones: C is that product of two F16 values, 22 bits, rounded
+    # once
+    x, a, b, ids, _, _ = lora_case(M, 40, K, 8, 1, "f16", [0] * M, 96, residual=False)
+    a[:], b[:] = 0, 0
+    a[0, 0, 3], a[0, 1, 9], b[0, :, 1] = 64.0, 1.3701 * 2.0 ** -8, 1.0
+    x[:, 3], x[:, 9] = 64.0, 1 + torch.arange(M) / 37
+    got = lora_run(x, a, b, ids, None, None, "f16").cpu()
+    assert torch.equal(got, (x[:, 9].double() * a[0, 1, 9].double()).half()[:, None].expand(M, 40))
+
+
 @pytest.mark.parametrize("head_dim,cache", [(64, "f16"), (128, "f16"), (64, "fp8"), (128, "fp8")])
 def test_attend_small_weights_beside_large_ones(head_dim, cache):
     # every 16th key has e^11 to e^13 times the weight of each other, but zeros
