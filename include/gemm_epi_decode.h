@@ -71,7 +71,8 @@ gemm_epi_status gemm_epi_rmsnorm(const void* X, int64_t ldx, const void* R, int6
  * dimension); nothing else may overlap C or the workspace.  The inner
  * product X A^T is kept in fp32; it enters the second product as two
  * 16-bit parts of each row scaled by a power of two (16 significant bits in
- * BF16, 22 in F16); sums in fp32, one rounding.
+ * BF16, 22 in F16); sums in fp32, one rounding.  What meets an infinity of B is
+ * an infinity or NaN.
  * workspace: gemm_epi_lora_workspace_size bytes, 16-byte aligned, with no
  * content of its own before or after a call; calls that share it must not
  * overlap in time.
@@ -170,7 +171,8 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
  *     O[i, h] = sum_j softmax_j(Q[i, h] . K_j / sqrt(head_dim)) V_j
  *
  * over the tokens j < lens[i] of sequence i whose page exists, with K_j and
- * V_j of key head h / (q_heads / heads).  No such token: O[i, h] = 0.
+ * V_j of key head h / (q_heads / heads).  No such token, or only minus infinities
+ * for scores: O[i, h] = 0.
  *   Q   [batch, q_heads, head_dim], ldq elements between sequences, format
  *       `dtype` (F16 or BF16), that of the cache unless that is FP8_E4M3
  *   O   [batch, q_heads, head_dim], ldo elements between sequences, `dtype`
@@ -181,9 +183,10 @@ gemm_epi_status gemm_epi_cache_append(const gemm_epi_paged_cache* cache, const g
  * second product as two 16-bit parts (their rounded value and its rounded
  * remainder), in F16 of 2^7 times their ratio to the largest, in BF16 and for
  * an FP8_E4M3 cache in BF16; such a cache's values enter both products exactly
- * (from 2^128 on as infinities); O is rounded once.  The keys are split over
- * workgroups by the lengths found on the device and joined in a fixed order:
- * the same inputs give the same bits.
+ * (from 2^128 on as infinities); O is rounded once.  What attends to an
+ * infinity of V is an infinity or NaN.  The keys are split over workgroups by
+ * the lengths found on the device and joined in a fixed order: the same inputs
+ * give the same bits.
  * workspace: gemm_epi_attention_decode_workspace_size bytes, 16-byte aligned.
  * Its first GEMM_EPI_ATTENTION_DECODE_COUNTER_BYTES hold counters: zero-filled
  * once before its first use, and left zero by every run that completes; the
