@@ -19,10 +19,12 @@ CALLS_PATH = os.path.join(_HERE, "_calls.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "gemm_epi.h")
 
 # Enum values of include/gemm_epi.h
-DTYPES = {"f16": 0, "bf16": 1, "f32": 2, "fp8": 3}
+DTYPES = {"f16": 0, "bf16": 1, "f32": 2, "fp8": 3, "i8": 4}
 LAYOUTS = {"row": 0, "col": 1}
 EPILOGUES = {"none": 0, "relu": 1, "bias_relu": 2, "bias_gelu": 3, "bias": 4, "silu": 5, "bias_silu": 6}
 KERNELS = {"auto": 0, "generic": 1, "tile": 2, "skinny": 3}
+SCORES = {"softmax": 0, "sigmoid": 1}  # include/gemm_epi_experts.h
+GATHER, SCATTER, GATED = 1, 2, 4
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_HIP", 4: "ERR_NO_MEMORY"}
 OK = 0
@@ -45,6 +47,12 @@ class _PageTable(ctypes.Structure):
     """struct gemm_epi_page_table (include/gemm_epi_decode.h)."""
     _fields_ = [("pages", ctypes.c_void_p), ("ld", ctypes.c_int64), ("width", ctypes.c_int64),
                 ("lens", ctypes.c_void_p), ("batch", ctypes.c_int64)]
+
+
+class _Groups(ctypes.Structure):
+    """struct gemm_epi_groups (include/gemm_epi_experts.h)."""
+    _fields_ = [("offsets", ctypes.c_void_p), ("order", ctypes.c_void_p), ("groups", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("per", ctypes.c_int64)]
 
 
 class GemmEpiError(RuntimeError):
@@ -124,6 +132,20 @@ def load_library(path: str = LIB_PATH):
     lib.gemm_epi_attention_decode.restype = i32
     lib.gemm_epi_attention_decode_workspace_size.argtypes = [pc, i64, i64, i64]
     lib.gemm_epi_attention_decode_workspace_size.restype = sz
+    # the experts' feed-forward and 8-bit products (include/gemm_epi_experts.h)
+    lib.gemm_epi_quantise_i8.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, vp]
+    lib.gemm_epi_quantise_i8.restype = i32
+    lib.gemm_epi_i8_gemm.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp]
+    lib.gemm_epi_i8_gemm.restype = i32
+    lib.gemm_epi_route.argtypes = [vp, i64, i32, i64, i64, i64, i32, i32, f32, vp, vp, vp, vp, vp]
+    lib.gemm_epi_route.restype = i32
+    lib.gemm_epi_group_rows.argtypes = [vp, i64, i64, vp, vp, vp]
+    lib.gemm_epi_group_rows.restype = i32
+    lib.gemm_epi_grouped_gemm.argtypes = [ctypes.POINTER(_Groups), vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i32,
+                                          i32, i32, i32, vp]
+    lib.gemm_epi_grouped_gemm.restype = i32
+    lib.gemm_epi_combine.argtypes = [vp, i64, vp, vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, vp]
+    lib.gemm_epi_combine.restype = i32
     # measurement helpers (include/gemm_epi_probes.h)
     lib.gemm_epi_probe_hbm_read.argtypes = [vp, ctypes.c_size_t, vp, vp]
     lib.gemm_epi_probe_hbm_read.restype = i32
@@ -472,6 +494,120 @@ class PagedCache:
             st = C.m.attend(index, s, *args, _workspace(-st, stream, ATTENTION_DECODE_COUNTER_BYTES))
         if st != OK:
             raise GemmEpiError("gemm_epi_attention_decode", st)
+
+
+# ---- the experts' feed-forward and 8-bit products (include/gemm_epi_experts.h) ----
+
+def gemm_epi_quantise_i8(X, ldx, Y, ldy, scale, rows, cols, dtype, stream) -> int:
+    return load_library().gemm_epi_quantise_i8(X, ldx, Y, ldy, scale, rows, cols, DTYPES[dtype], stream)
+
+
+def gemm_epi_i8_gemm(A, lda, a_scale, B, ldb, b_scale, bias, R, ldr, C, ldc, M, N, K, epilogue, out_dtype,
+                     stream) -> int:
+    return load_library().gemm_epi_i8_gemm(A, lda, a_scale, B, ldb, b_scale, bias, R, ldr, C, ldc, M, N, K,
+                                           EPILOGUES[epilogue], DTYPES[out_dtype], stream)
+
+
+def gemm_epi_route(logits, ldl, dtype, tokens, experts, per, score, renormalise, scale, ids, weights, offsets, order,
+                   stream) -> int:
+    return load_library().gemm_epi_route(logits, ldl, DTYPES[dtype], tokens, experts, per, SCORES[score],
+                                         int(bool(renormalise)), scale, ids, weights, offsets, order, stream)
+
+
+def gemm_epi_group_rows(ids, rows, groups, offsets, order, stream) -> int:
+    return load_library().gemm_epi_group_rows(ids, rows, groups, offsets, order, stream)
+
+
+def groups_struct(offsets, order, groups, rows, per):
+    """A gemm_epi_groups of pointers and sizes (for the call below)."""
+    return _Groups(offsets, order, groups, rows, per)
+
+
+def gemm_epi_grouped_gemm(groups, X, ldx, x_scale, W, w_scale, bias, C, ldc, N, K, flags, epilogue, dtype, out_dtype,
+                          stream) -> int:
+    return load_library().gemm_epi_grouped_gemm(groups, X, ldx, x_scale, W, w_scale, bias, C, ldc, N, K, flags,
+                                                EPILOGUES[epilogue], DTYPES[dtype], DTYPES[out_dtype], stream)
+
+
+def gemm_epi_combine(Z, ldz, weights, ids, experts, R, ldr, Y, ldy, tokens, per, cols, dtype, stream) -> int:
+    return load_library().gemm_epi_combine(Z, ldz, weights, ids, experts, R, ldr, Y, ldy, tokens, per, cols,
+                                           DTYPES[dtype], stream)
+
+
+def _called(fn, name, stream, *args):
+    """A call of _calls.so on the current device and the given or torch's
+    current stream."""
+    C = _Calls
+    if C.m is None:
+        _load_calls()
+    index = C.device()
+    st = getattr(C.m, fn)(index, C.raw(index) if stream is None else _stream_of(stream, index), *args)
+    if st != OK:
+        raise GemmEpiError(name, st)
+
+
+def quantise_i8(x, y, scale, stream=None):
+    """scale = max(max|x| / 127, 2^-100), y = x / scale rounded to the nearest
+    integer, over the last axis of x [rows, cols] float16 or bfloat16 and y
+    [rows, cols] int8 (rows may be strided); scale [rows] float32.  A row that
+    holds an infinity or a NaN gets scale NaN.  Enqueued on torch's current
+    stream (or `stream`), not synchronised, as all calls below."""
+    _called("quantise_i8", "gemm_epi_quantise_i8", stream, x, y, scale)
+
+
+def i8_gemm(a, a_scale, b, b_scale, c, bias=None, residual=None, epilogue="none", stream=None):
+    """c = act((a b^T) a_scale[:, None] b_scale[None] + bias) + residual for
+    int8 rows a [M, K] and weights b [N, K], a_scale [M] and b_scale [N]
+    float32; c and residual [M, N] float16 or bfloat16 (``residual`` may be
+    ``c`` itself), bias [N] of that format for an epilogue with one.  Rows may
+    be strided.  ``epilogue``: a name of EPILOGUES."""
+    _called("i8_gemm", "gemm_epi_i8_gemm", stream, a, a_scale, b, b_scale, c, bias, residual, EPILOGUES[epilogue])
+
+
+def route(logits, ids, weights, score="softmax", renormalise=True, scale=1.0, offsets=None, order=None, stream=None):
+    """The experts of each token: ids [tokens, per] int32 of the largest
+    logits [tokens, experts] (float32, float16 or bfloat16, rows may be
+    strided), of equal ones the lower first, and their weights [tokens, per]
+    float32: the softmax over all experts or each logit's sigmoid
+    (``score``), divided by its sum over the chosen ones (``renormalise``), times
+    ``scale``.  An expert at minus infinity or NaN is not chosen: id -1, weight
+    0.  With ``offsets`` [experts + 1] and ``order`` [tokens * per] int32, those
+    of ``group_rows`` too."""
+    _called("route", "gemm_epi_route", stream, logits, ids, weights, SCORES[score], bool(renormalise), scale, offsets,
+            order)
+
+
+def group_rows(ids, offsets, order, stream=None):
+    """The entries of ids (int32, contiguous) by group: order [entries] int32
+    holds their numbers, group by group and ascending in each, those of group
+    g from offsets[g] to offsets[g + 1] - 1 (offsets [groups + 1] int32); an id
+    outside [0, groups) is in no group, and as many -1 stand behind the last."""
+    _called("group_rows", "gemm_epi_group_rows", stream, ids, offsets, order)
+
+
+def grouped_gemm(x, w, c, offsets, order=None, per=1, gather=False, scatter=False, gated=False, bias=None,
+                 epilogue="none", x_scale=None, w_scale=None, stream=None):
+    """For place i of group g, offsets[g] <= i < offsets[g + 1], and entry q =
+    order[i] (without ``order``: i): row q of c (``scatter``, else row i) = act(row
+    q // per of x (``gather``, else row i) w[g]^T + bias[g]).  w [groups, N, K],
+    and with ``gated`` [groups, 2 N, K], N rows of gates, then N of values: act(x
+    gate^T + bias) * (x value^T + bias).  c [rows, N], x [rows, K], or with ``gather``
+    [rows / per, K] (rows may be strided), bias [groups, N or 2 N].  x, w, c and
+    bias of one 16-bit format, or x and w int8 with x_scale [rows of x] and
+    w_scale [groups, N or 2 N] float32.  Rows of c that no place writes are left
+    as they were."""
+    _called("grouped_gemm", "gemm_epi_grouped_gemm", stream, x, w, c, offsets, order, per,
+            (GATHER if gather else 0) | (SCATTER if scatter else 0) | (GATED if gated else 0), bias,
+            EPILOGUES[epilogue], x_scale, w_scale)
+
+
+def combine(z, weights, ids, y, experts, residual=None, stream=None):
+    """y[t] = residual[t] + the sum over j of weights[t, j] z[t * per + j], over
+    the j with 0 <= ids[t, j] < experts (``ids`` None: all).  z [tokens * per,
+    cols], y and residual [tokens, cols] of one 16-bit format (rows may be
+    strided; ``residual`` may be ``y`` itself), weights [tokens, per] float32, ids
+    [tokens, per] int32."""
+    _called("combine", "gemm_epi_combine", stream, z, weights, ids, y, experts, residual)
 
 
 # ---- measurement helpers (include/gemm_epi_probes.h) -------------------------

@@ -38,7 +38,8 @@
 extern "C" {
 #endif
 
-/* Element formats.  F32 and FP8_E4M3 are output formats only.  FP8_E4M3 is
+/* Element formats.  F32 and FP8_E4M3 are output formats only, I8 is of the
+ * products of gemm_epi_experts.h only.  FP8_E4M3 is
  * the OCP 8-bit floating-point E4M3 format (bias 7, no infinities, largest
  * finite 448): the quantised output the tutorial lists among the fusions
  * (csdn ch.10 sec. 10.7, "GEMM + quantisation").  Conversion to it
@@ -47,7 +48,8 @@ typedef enum gemm_epi_dtype {
   GEMM_EPI_F16 = 0,      /* IEEE binary16 */
   GEMM_EPI_BF16 = 1,     /* bfloat16 (top half of binary32) */
   GEMM_EPI_F32 = 2,      /* IEEE binary32 */
-  GEMM_EPI_FP8_E4M3 = 3  /* OCP FP8 E4M3, one byte */
+  GEMM_EPI_FP8_E4M3 = 3, /* OCP FP8 E4M3, one byte */
+  GEMM_EPI_I8 = 4        /* 8-bit signed integer */
 } gemm_epi_dtype;
 
 /* Storage order of an R x C operand: ROW_MAJOR puts (r, c) at r*C + c,
