@@ -28,6 +28,8 @@ bool too_many(int64_t rows, int64_t groups, int64_t cols) {
 
 // Bytes between rows: a tile's rows are at 32-bit offsets from its first.
 constexpr int64_t kMaxPitch = (int64_t)1 << 24;
+// Bytes of a group's gates: the values' rows are at 32-bit offsets from them.
+constexpr int64_t kMaxGate = (int64_t)1 << 31;
 
 }  // namespace
 }  // namespace grouped
@@ -83,7 +85,7 @@ gemm_epi_status gemm_epi_grouped_gemm(const gemm_epi_groups* groups, const void*
   for (const int64_t n : {g.rows, g.per, N, ldc})
     if (n >= kLim) return GEMM_EPI_ERR_UNSUPPORTED;
   const int64_t size = i8 ? 1 : 2, cols = gated ? 2 * N : N;
-  if (K * size % 16 != 0 || K >= (1 << 17) || ldx * size % 16 != 0 || ldx * size > kMaxPitch || g.groups > 1024 || cols >= kLim ||
+  if ((gated && N * K * size > kMaxGate) || K * size % 16 != 0 || K >= (1 << 17) || ldx * size % 16 != 0 || ldx * size > kMaxPitch || g.groups > 1024 || cols >= kLim ||
       too_many(g.rows, g.groups, cols) || (gather && g.rows / g.per * ldx * size >= (int64_t)0xffff0000))
     return GEMM_EPI_ERR_UNSUPPORTED;
   if (g.rows == 0) return GEMM_EPI_OK;
