@@ -30,6 +30,10 @@ struct Args {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
+// (an access off its alignment is one instruction all the same)
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
 template <typename T>
 struct Elem {
   static constexpr bool kInt = __is_same(T, int8_t);
@@ -142,80 +146,6 @@ __device__ __forceinline__ int column_of(int r) {
 }
 
 // ---------------------------------------------------------------------------
-// a simple kernel: tiles of 64 x 64, one stage through registers
-// ---------------------------------------------------------------------------
-template <typename T, typename TOut, bool GATED>
-__global__ __launch_bounds__(256) void simple_kernel(Args a) {
-  constexpr int BM = 64, BN = 64, ROW = 128, LD = ROW + 16;
-  constexpr int ES = sizeof(T), OUT = GATED ? BN / 2 : BN;
-  __shared__ __attribute__((aligned(16))) char sa[BM * LD], sb[BN * LD];
-  __shared__ int xrow[BM], crow[BM];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Found f = find_tile<BM, 4>(a, blockIdx.x, lane);
-  if (f.group < 0) return;
-  if (tid < BM) {
-    const int i = f.begin + tid, q = i < f.end ? entry_of(a, i) : -1;
-    xrow[tid] = q < 0 ? -1 : a.gather ? q / a.per : i;
-    crow[tid] = q < 0 ? -1 : a.scatter ? q : i;
-  }
-  __syncthreads();
-  const int wm = wave >> 1, wn = wave & 1, c = lane & 15, h = lane >> 4;
-  typename Elem<T>::acc acc[2][2] = {};
-  const char* w = (const char*)a.W + f.group * a.group_w * ES;
-  const int64_t row_bytes = (int64_t)a.K * ES;
-  for (int64_t k0 = 0; k0 < row_bytes; k0 += ROW) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int piece = tid + 256 * p, r = piece >> 3, at = (piece & 7) * 16;
-      u32x4 x = {}, y = {};
-      if (k0 + at < row_bytes) {
-        if (xrow[r] >= 0) x = *(const u32x4*)((const char*)a.X + xrow[r] * a.ldx * ES + k0 + at);
-        const int n = f.tn * OUT + column_of<GATED>(r);
-        if (n < a.N) y = *(const u32x4*)(w + (int64_t)(n + (GATED && (r & 16) ? a.N : 0)) * a.ldw * ES + k0 + at);
-      }
-      *(u32x4*)(sa + r * LD + at) = x;
-      *(u32x4*)(sb + r * LD + at) = y;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = mfma<T>(*(const u32x4*)(sb + (wn * 32 + j * 16 + c) * LD + kk * 64 + h * 16),
-                              *(const u32x4*)(sa + (wm * 32 + i * 16 + c) * LD + kk * 64 + h * 16), acc[i][j]);
-    __syncthreads();
-  }
-  with_activation(a.epi, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = wm * 32 + i * 16 + c;
-    if (crow[r] < 0) continue;
-    const float xs = Elem<T>::kInt ? a.xs[xrow[r]] : 1.0f;
-    TOut* out = (TOut*)a.C + crow[r] * a.ldc;
-    // the columns of a block of this wave, before the epilogue's end
-    auto value = [&](int j, int e, int n) __attribute__((always_inline)) {
-      const int64_t at = (int64_t)f.group * a.N * (GATED ? 2 : 1) + (GATED && (j & 1) ? a.N : 0) + n;
-      float z = (float)acc[i][j][e];
-      if constexpr (Elem<T>::kInt) z = z * xs * a.ws[at];
-      return has_bias(a.epi) ? z + to_f32(((const TOut*)a.bias)[at]) : z;
-    };
-#pragma unroll
-    for (int j = 0; j < 2; j += GATED ? 2 : 1)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int n = f.tn * OUT + column_of<GATED>(wn * 32 + j * 16) + 4 * h + e;
-        if (n >= a.N) continue;
-        float v = activated<decltype(act)::value>(value(j, e, n));
-        if constexpr (GATED) v *= value(j + 1, e, n);
-        else if (a.R) v += to_f32(((const TOut*)a.R)[crow[r] * a.ldr + n]);
-        out[n] = from_f32<TOut>(v);
-      }
-  }  });
-}
-
-// ---------------------------------------------------------------------------
 // the tile kernel
 // ---------------------------------------------------------------------------
 using tile::kRowBytes;
@@ -228,7 +158,7 @@ using tile::lds_ptr;
 // instruction, past the buffer's end (zeros, no access) for a row that is none.
 // The k axis is shifted by `pad` bytes, so that the last k-steps are whole and
 // the chunks of the first before K's beginning load as zeros.
-template <int R, int NW>
+template <int R, int NW, int AUX = 0>
 struct RowLoader {
   static constexpr int NI = R / (8 * NW);
   static_assert(NI >= 1 && NI <= 8 && R % (8 * NW) == 0, "whole instructions");
@@ -251,11 +181,11 @@ struct RowLoader {
   }
   __device__ __forceinline__ void issue(char* dst, int kt, int i) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(dst + (NW * i + wave) * 1024), 16, voff[i],
-                                             kt * kRowBytes, 0, 0);
+                                             kt * kRowBytes, 0, AUX);
   }
   __device__ __forceinline__ void issue_first(char* dst, int kt, int i, int pad) const {
     const uint32_t v = 16 * chunk + kt * kRowBytes < pad ? 0xFFFFFFF0u : voff[i];
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(dst + (NW * i + wave) * 1024), 16, v, kt * kRowBytes, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)(dst + (NW * i + wave) * 1024), 16, v, kt * kRowBytes, 0, AUX);
   }
 };
 
@@ -267,17 +197,19 @@ struct Edges {
   f32x4 ws[BN / 4], bias[BN / 4];  // of each row of the tile of W
 };
 
-// The tile's rows of X, -1 for none, are left in xrow.
+// By 256 threads, thread r with the entry q of row r (-1: none).  The tile's rows
+// of X, -1 for none, are left in xrow.
 template <typename T, typename TOut, bool GATED, int BM, int BN>
-__device__ __forceinline__ void fill_edges(const Args& a, const Found& f, Edges<BM, BN>& edges, int* xrow, int tid, int threads) {
-  for (int r = tid; r < BM; r += threads) {
-    const int i = f.begin + r, q = i < f.end ? entry_of(a, i) : -1, x = q < 0 ? -1 : a.gather ? q / a.per : i;
-    xrow[r] = x;
-    edges.c[r] = q < 0 ? -1 : a.scatter ? q : i;
-    if constexpr (Elem<T>::kInt) edges.xs[r] = q < 0 ? 0.0f : a.xs[x];
+__device__ __forceinline__ void fill_edges(const Args& a, const Found& f, Edges<BM, BN>& edges, int* xrow, int tid, int q) {
+  static_assert(BM <= 256 && BN <= 256, "a thread a row");
+  if (tid < BM) {
+    const int i = f.begin + tid, x = q < 0 ? -1 : a.gather ? q / a.per : i;
+    xrow[tid] = x;
+    edges.c[tid] = q < 0 ? -1 : a.scatter ? q : i;
+    if constexpr (Elem<T>::kInt) edges.xs[tid] = q < 0 ? 0.0f : a.xs[x];
   }
   const bool biased = has_bias(a.epi);
-  for (int r = tid; r < BN; r += threads) {
+  if (const int r = tid; r < BN) {
     const int n = f.tn * (GATED ? BN / 2 : BN) + column_of<GATED>(r);
     const int64_t at = (int64_t)f.group * a.N * (GATED ? 2 : 1) + (GATED && (r & 16) ? a.N : 0) + n;
     if constexpr (Elem<T>::kInt) ((float*)edges.ws)[r] = n < a.N ? a.ws[at] : 0.0f;
@@ -285,49 +217,71 @@ __device__ __forceinline__ void fill_edges(const Args& a, const Found& f, Edges<
   }
 }
 
+// Four values of a row of the residual, those past the last column zeros.
+template <typename TOut>
+__device__ __forceinline__ u32x2 residual4(const TOut* r, int n, int N) {
+  if (n + 4 <= N) return *(const u32x2_any*)r;
+  u32x2 w = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < N) w[e >> 1] |= (uint32_t)bits16(r[e]) << (16 * (e & 1));
+  return w;
+}
+
 // Epilogue of a wave's TM x TN blocks of 16 x 16 (lane (c, h) has columns 4 h
 // .. + 3 of row c of each), rows r0 .. and W's rows w0 .. of the tile, output
 // columns n0 ..: the scales, bias, activation, gate's product or residual in
 // fp32, one rounding, then each band of 16 rows through the wave's own LDS
-// (16-byte chunks swizzled by row) and out in 16-byte pieces along rows.
-template <typename T, typename TOut, bool GATED, int ACT, int TM, int TN, int BM, int BN>
+// (16-byte chunks swizzled by row) and out in 16-byte pieces along rows.  What
+// belongs to columns is read once, a band's residual while the band before it
+// is worked on.
+template <typename T, typename TOut, bool GATED, int ACT, bool RES, int TM, int TN, int BM, int BN>
 __device__ __forceinline__ void write_rows(const Args& a, const typename Elem<T>::acc (&acc)[TM][TN],
                                            const Edges<BM, BN>& edges, int r0, int w0, int n0, int lane, char* stage) {
   constexpr int W = (GATED ? TN / 2 : TN) * 16;   // output columns
   constexpr int CPR = W * 2 / 16, SWM = (CPR < 16 ? CPR : 16) - 1, RPI = 64 / CPR < 16 ? 64 / CPR : 16;
   constexpr int S = GATED ? 2 : 1;
   const int c = lane & 15, h = lane >> 4;
+  f32x4 ws[Elem<T>::kInt ? TN : 1], bias[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    if constexpr (Elem<T>::kInt) ws[j] = edges.ws[w0 / 4 + 4 * j + h];
+    bias[j] = edges.bias[w0 / 4 + 4 * j + h];
+  }
+  u32x2 res[RES ? 2 : 1][RES ? TN : 1];
+  auto load_residual = [&](int i, u32x2 (&r)[RES ? TN : 1]) __attribute__((always_inline)) {
+    const int to = edges.c[r0 + 16 * i + c];
+    if (to < 0) return;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int n = n0 + 16 * j + 4 * h;
+      r[j] = residual4((const TOut*)a.R + to * a.ldr + n, n, a.N);
+    }
+  };
+  if constexpr (RES) load_residual(0, res[0]);
   static_for<TM>([&](auto i_c) __attribute__((always_inline)) {
     constexpr int i = decltype(i_c)::value;
     const int row = r0 + 16 * i;
     const float xs = Elem<T>::kInt ? edges.xs[row + c] : 1.0f;
-    const int to = edges.c[row + c];
+    if constexpr (RES && i + 1 < TM) load_residual(i + 1, res[(i + 1) & 1]);
     static_for<TN / S>([&](auto j_c) __attribute__((always_inline)) {
       constexpr int j = decltype(j_c)::value;
       auto z = [&](auto jj_c) __attribute__((always_inline)) {
         constexpr int jj = decltype(jj_c)::value;
-        const int at = w0 / 4 + 4 * jj + h;
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][jj][e];
-        if constexpr (Elem<T>::kInt) v = v * xs * edges.ws[at];
-        return v + edges.bias[at];
+        if constexpr (Elem<T>::kInt) v = v * xs * ws[jj];
+        return v + bias[jj];
       };
-      const int n = n0 + j * 16 + 4 * h;
       f32x4 v = z(std::integral_constant<int, S * j>{});
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = activated<ACT>(v[e]);
-      if constexpr (GATED) {
-        v *= z(std::integral_constant<int, 2 * j + 1>{});
-      } else if (a.R && to >= 0) {
-        const TOut* r = (const TOut*)a.R + to * a.ldr + n;
-        if (n + 4 <= a.N && ((uintptr_t)r & 7u) == 0) {
-          v += load4<TOut>(r);
-        } else {
+      if constexpr (GATED) v *= z(std::integral_constant<int, 2 * j + 1>{});
+      if constexpr (RES) {
+        const u32x2 w = res[i & 1][j];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) v[e] += to_f32(r[e]);
-        }
+        for (int e = 0; e < 4; ++e) v[e] += to_f32(__builtin_bit_cast(TOut, (uint16_t)(w[e >> 1] >> (16 * (e & 1)))));
       }
       const int chunk = 2 * j + (h >> 1);
       *(u32x2*)(stage + c * (W * 2) + ((chunk ^ (c & SWM)) << 4) + 8 * (h & 1)) =
@@ -338,62 +292,76 @@ __device__ __forceinline__ void write_rows(const Args& a, const typename Elem<T>
     for (int t = 0; t < 16 / RPI; ++t) {
       const int r = t * RPI + lane / CPR, ch = lane % CPR;
       if (RPI * CPR < 64 && lane >= RPI * CPR) continue;
-      const u32x4 d = *(const u32x4*)(stage + r * (W * 2) + ((ch ^ (r & SWM)) << 4));
+      const char* src = stage + r * (W * 2) + ((ch ^ (r & SWM)) << 4);
       const int cr = edges.c[row + r], n = n0 + 8 * ch;
       if (cr < 0 || n >= a.N) continue;
       uint16_t* dst = (uint16_t*)a.C + cr * a.ldc + n;
-      if (n + 8 <= a.N && ((uintptr_t)dst & 15u) == 0) {
-        *(u32x4*)dst = d;
+      if (n + 8 <= a.N) {
+        *(u32x4_any*)dst = *(const u32x4*)src;
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < a.N) dst[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+#pragma unroll 1
+        for (int e = 0; e < a.N - n; ++e) dst[e] = ((const uint16_t*)src)[e];
       }
     }
     __builtin_amdgcn_sched_barrier(0);
   });
 }
 
-// BM x BN products (BN / 2 gated outputs) by 2 x 2 waves, in two LDS stages of
-// 128 bytes of K: the pipeline of gemm_tile16.hpp, of which a k-step is two
-// substeps of 64 bytes.
-template <typename T, typename TOut, bool GATED, int BM, int BN>
-__global__ __launch_bounds__(256) void tile_kernel(Args a) {
-  constexpr int NW = 4, WM = BM / 2, WN = BN / 2, TM = WM / 16, TN = WN / 16, OUT = GATED ? BN / 2 : BN;
+// Stage J of a ring: an object of its own, so that the compiler can tell a read
+// of one stage from a copy in flight into another (of one array of all stages,
+// it waits for every copy before a read: 229 us for 184).
+template <int J, int BYTES>
+__device__ __forceinline__ char* ring_stage() {
+  __shared__ __attribute__((aligned(1024))) char stage[BYTES];
+  return stage;
+}
+
+// BM x BN products (BN / 2 gated outputs) of tile f by WGM x 4 / WGM waves, in
+// a ring of P LDS stages (of STAGE bytes) of 128 bytes of K: the pipeline of
+// gemm_tile16.hpp, of which a k-step is two substeps of 64 bytes:
+//   substep 0   multiply the first half of tile kt, read its second;
+//   barrier     after this wave's copies of tile kt + 1 have landed: every wave
+//               is done reading tile kt's stage, tile kt + 1 is whole;
+//   substep 1   multiply the second half, read the first of tile kt + 1, and
+//               copy tile kt + P into the stage that tile kt leaves.
+template <typename T, typename TOut, bool GATED, int BM, int BN, int P, bool PAST, int WGM, int STAGE, int EM>
+__device__ __forceinline__ void multiply_tile(const Args& a, const Found& f, Edges<EM, BN>& edges, int* xrow, int tid) {
+  constexpr int NW = 4, WGN = NW / WGM, WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16, OUT = GATED ? BN / 2 : BN;
   constexpr int ES = sizeof(T);
   constexpr int A_BYTES = BM * kRowBytes, B_BYTES = BN * kRowBytes;
-  __shared__ __attribute__((aligned(1024))) char sA0[A_BYTES];
-  __shared__ __attribute__((aligned(1024))) char sA1[A_BYTES];
-  __shared__ __attribute__((aligned(1024))) char sB0[B_BYTES];
-  __shared__ __attribute__((aligned(1024))) char sB1[B_BYTES];
-  __shared__ int xrow[BM];
-  __shared__ Edges<BM, BN> edges;
-  struct Stage {
-    char* a;
-    char* b;
-  };
-  const Stage stage0{sA0, sB0}, stage1{sA1, sB1};
-  const int tid = threadIdx.x, lane = tid & 63;
+  static_assert(A_BYTES + B_BYTES <= STAGE && BM <= EM, "the stage holds the tile");
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / 2, wn = wave % 2;
-  const Found f = find_tile<BM, 4>(a, blockIdx.x, lane);
-  if (f.group < 0) return;
-  fill_edges<T, TOut, GATED>(a, f, edges, xrow, tid, 256);
-  __syncthreads();
+  const int wm = wave / WGN, wn = wave % WGN;
 
-  const int row_bytes = a.K * ES, KT = max(2, (row_bytes + kRowBytes - 1) / kRowBytes), pad = KT * kRowBytes - row_bytes;
+  // (the first k-steps hold what is missing to a multiple of P)
+  const int row_bytes = a.K * ES, rounds = (row_bytes + P * kRowBytes - 1) / (P * kRowBytes);
+  const int pad = rounds * P * kRowBytes - row_bytes;
   const int64_t xpitch = a.ldx * ES, wpitch = a.ldw * ES;
-  // X from its first row where rows are gathered, else from the tile's
-  const int x0 = a.gather ? 0 : f.begin, n0 = f.tn * OUT;
-  const RowLoader<BM, NW> la((const char*)a.X + x0 * xpitch, (a.gather ? a.rows / a.per : a.rows - x0) * xpitch, pad, tid,
-                             [&](int r) __attribute__((always_inline)) {
-                               return xrow[r] < 0 ? (int64_t)-1 : (xrow[r] - x0) * xpitch;
-                             });
-  const RowLoader<BN, NW> lb((const char*)a.W + f.group * a.group_w * ES + n0 * wpitch,
+  constexpr int NDA = RowLoader<BM, NW>::NI, NDB = RowLoader<BN, NW>::NI, NDL = NDA + NDB;
+  const int q = tid < BM && f.begin + tid < f.end ? entry_of(a, f.begin + tid) : -1;
+  const int n0 = f.tn * OUT;
+  const RowLoader<BN, NW, PAST ? 2 : 0> lb((const char*)a.W + f.group * a.group_w * ES + n0 * wpitch,
                              ((GATED ? 2 : 1) * (int64_t)a.N - n0) * wpitch, pad, tid,
                              [&](int r) __attribute__((always_inline)) {
                                const int n = column_of<GATED>(r);
                                return n0 + n < a.N ? (n + (GATED && (r & 16) ? (int64_t)a.N : 0)) * wpitch : (int64_t)-1;
+                             });
+  auto first_b = [&](auto j) __attribute__((always_inline)) {
+    constexpr int J = decltype(j)::value;
+#pragma unroll
+    for (int d = 0; d < NDB; ++d) lb.issue_first(ring_stage<J, STAGE>() + A_BYTES, J, d, pad);
+  };
+  // With two stages W's first copies are on their way while the rows of X are
+  // looked up (with more, the loop's waits count copies tile by tile).
+  if constexpr (P == 2) static_for<P>(first_b);
+  fill_edges<T, TOut, GATED>(a, f, edges, xrow, tid, q);
+  __syncthreads();
+  // X from its first row where rows are gathered, else from the tile's
+  const int x0 = a.gather ? 0 : f.begin;
+  const RowLoader<BM, NW> la((const char*)a.X + x0 * xpitch, (a.gather ? a.rows / a.per : a.rows - x0) * xpitch, pad, tid,
+                             [&](int r) __attribute__((always_inline)) {
+                               return xrow[r] < 0 ? (int64_t)-1 : (xrow[r] - x0) * xpitch;
                              });
 
   // Fragment rows w0 + 16 f + lane % 16 have the swizzle lane % 8: one offset
@@ -407,148 +375,279 @@ __global__ __launch_bounds__(256) void tile_kernel(Args a) {
   }
   typename Elem<T>::acc acc[TM][TN] = {};
   u32x4 fa[2][TM], fb[2][TN];
-  auto read_frag = [&](const Stage& st, int kk, int f, u32x4 (&xa)[TM], u32x4 (&xb)[TN]) __attribute__((always_inline)) {
-    if (f < TN) xb[f] = *(const u32x4*)(st.b + boff[kk] + f * 16 * kRowBytes);
-    else xa[f - TN] = *(const u32x4*)(st.a + aoff[kk] + (f - TN) * 16 * kRowBytes);
+  auto read_frag = [&](auto slot_c, int kk, int f, u32x4 (&xa)[TM], u32x4 (&xb)[TN]) __attribute__((always_inline)) {
+    constexpr int S = decltype(slot_c)::value;
+    char* const st = ring_stage<S, STAGE>();
+    if (f < TN) xb[f] = *(const u32x4*)(st + A_BYTES + boff[kk] + f * 16 * kRowBytes);
+    else xa[f - TN] = *(const u32x4*)(st + aoff[kk] + (f - TN) * 16 * kRowBytes);
   };
-  constexpr int NMF = TM * TN, NDR = TM + TN, NDA = RowLoader<BM, NW>::NI, NDL = NDA + RowLoader<BN, NW>::NI;
-  auto substep = [&](auto sub_c, const u32x4 (&xa)[TM], const u32x4 (&xb)[TN], const Stage& rd, int rd_kk, bool do_read,
-                     u32x4 (&na)[TM], u32x4 (&nb)[TN], const Stage& to, bool do_copy, int kt) __attribute__((always_inline)) {
-    constexpr int sub = decltype(sub_c)::value;
+  constexpr int NMF = TM * TN, NDR = TM + TN;
+  // NMF slots of one product and its share of the reads and copies; nothing
+  // moves across a slot's end.
+  auto substep = [&](auto sub_c, const u32x4 (&xa)[TM], const u32x4 (&xb)[TN], auto rd, int rd_kk, auto do_read,
+                     u32x4 (&na)[TM], u32x4 (&nb)[TN], auto to, auto do_copy, int kt) __attribute__((always_inline)) {
+    constexpr int sub = decltype(sub_c)::value, S = decltype(to)::value;
     static_for<NMF>([&](auto slot_c) __attribute__((always_inline)) {
       constexpr int slot = decltype(slot_c)::value, i = slot / TN, j = slot % TN;
       acc[i][j] = mfma<T>(xb[j], xa[i], acc[i][j]);
-      static_for<NDR>([&](auto r_c) __attribute__((always_inline)) {
-        constexpr int r = decltype(r_c)::value;
-        if constexpr (r * NMF / NDR == slot)
-          if (do_read) read_frag(rd, rd_kk, r, na, nb);
-      });
-      if constexpr (sub == 1) {
-        if (do_copy) {
-          static_for<NDL>([&](auto d_c) __attribute__((always_inline)) {
-            constexpr int d = decltype(d_c)::value;
-            if constexpr (d * NMF / NDL == slot) {
-              if constexpr (d < NDA) la.issue(to.a, kt + 2, d);
-              else lb.issue(to.b, kt + 2, d - NDA);
-            }
-          });
-        }
+      if constexpr (decltype(do_read)::value) {
+        static_for<NDR>([&](auto r_c) __attribute__((always_inline)) {
+          constexpr int r = decltype(r_c)::value;
+          if constexpr (r * NMF / NDR == slot) read_frag(rd, rd_kk, r, na, nb);
+        });
+      }
+      if constexpr (sub == 1 && decltype(do_copy)::value) {
+        static_for<NDL>([&](auto d_c) __attribute__((always_inline)) {
+          constexpr int d = decltype(d_c)::value;
+          if constexpr (d * NMF / NDL == slot) {
+            char* const st = ring_stage<S, STAGE>();
+            if constexpr (d < NDA) la.issue(st, kt + P, d);
+            else lb.issue(st + A_BYTES, kt + P, d - NDA);
+          }
+        });
       }
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  auto kstep = [&](const Stage& cur, const Stage& nxt, int kt, bool more1, bool more2) __attribute__((always_inline)) {
-    substep(std::integral_constant<int, 0>{}, fa[0], fb[0], cur, 1, true, fa[1], fb[1], cur, false, kt);
-    // this wave's copies of tile kt + 1 are its only outstanding ones
-    tile::kloop_barrier<0>();
+  // k-step kt = P round + J; the last round copies nothing more
+  auto kstep = [&](auto slot_c, auto last_c, int kt) __attribute__((always_inline)) {
+    constexpr int J = decltype(slot_c)::value;
+    constexpr bool LAST = decltype(last_c)::value;
+    constexpr std::integral_constant<int, J> cur{};
+    constexpr std::integral_constant<int, (J + 1) % P> nxt{};
+    substep(std::integral_constant<int, 0>{}, fa[0], fb[0], cur, 1, std::true_type{}, fa[1], fb[1], cur, std::false_type{}, kt);
+    // copies of tile kt + 2 and on may be outstanding
+    tile::kloop_barrier<NDL * (LAST ? (P - 2 - J > 0 ? P - 2 - J : 0) : P - 2)>();
     __builtin_amdgcn_sched_barrier(0);
-    substep(std::integral_constant<int, 1>{}, fa[1], fb[1], nxt, 0, more1, fa[0], fb[0], cur, more2, kt);
+    substep(std::integral_constant<int, 1>{}, fa[1], fb[1], nxt, 0, std::bool_constant<!(LAST && J == P - 1)>{}, fa[0], fb[0],
+            cur, std::bool_constant<!LAST>{}, kt);
   };
-  // Tile t lives in stage (t + KT) % 2: the last two k-steps are peeled.
-  auto prologue = [&](const Stage& first, const Stage& second) __attribute__((always_inline)) {
+  static_for<P>([&](auto j) __attribute__((always_inline)) {
+    constexpr int J = decltype(j)::value;
 #pragma unroll
-    for (int d = 0; d < NDL; ++d) {
-      if (d < NDA) la.issue_first(first.a, 0, d, pad);
-      else lb.issue_first(first.b, 0, d - NDA, pad);
-    }
+    for (int d = 0; d < NDA; ++d) la.issue_first(ring_stage<J, STAGE>(), J, d, pad);
+    if constexpr (P > 2) first_b(j);
+  });
+  tile::kloop_barrier<(P == 2 ? NDA : NDL * (P - 1))>();
 #pragma unroll
-    for (int d = 0; d < NDL; ++d) {
-      if (d < NDA) la.issue_first(second.a, 1, d, pad);
-      else lb.issue_first(second.b, 1, d - NDA, pad);
-    }
-    tile::kloop_barrier<NDL>();
-#pragma unroll
-    for (int f = 0; f < NDR; ++f) read_frag(first, 0, f, fa[0], fb[0]);
-  };
+  for (int f = 0; f < NDR; ++f) read_frag(std::integral_constant<int, 0>{}, 0, f, fa[0], fb[0]);
   int kt = 0;
-  if (KT & 1) {
-    prologue(stage1, stage0);
-    kstep(stage1, stage0, 0, true, true);
-    kt = 1;
-  } else {
-    prologue(stage0, stage1);
+  // (128 accumulators a lane and more: without a round before the loop they are copied
+  // between register files around every product)
+  if constexpr (NMF == 64 || WGM == 1) {
+    if (rounds > 1) {
+      static_for<P>([&](auto j) __attribute__((always_inline)) { kstep(j, std::false_type{}, decltype(j)::value); });
+      kt = P;
+    }
   }
-  for (; kt + 4 <= KT; kt += 2) {
-    kstep(stage0, stage1, kt, true, true);
-    kstep(stage1, stage0, kt + 1, true, true);
-  }
-  kstep(stage0, stage1, kt, true, false);
-  kstep(stage1, stage0, kt + 1, false, false);
+  for (; kt < (rounds - 1) * P; kt += P)
+    static_for<P>([&](auto j) __attribute__((always_inline)) { kstep(j, std::false_type{}, kt + decltype(j)::value); });
+  static_for<P>([&](auto j) __attribute__((always_inline)) { kstep(j, std::true_type{}, kt + decltype(j)::value); });
 
   // Every wave is done with the stages: their memory stages the outputs.
   __syncthreads();
-  static_assert(16 * WN * 2 <= A_BYTES && 16 * WN * 2 <= B_BYTES, "staging area");
-  char* const mine = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
+  static_assert(NW * 16 * WN * 2 <= A_BYTES + B_BYTES, "staging area");
+  char* const mine = ring_stage<0, STAGE>() + wave * (16 * WN * 2);
   with_activation(a.epi, [&](auto act) __attribute__((always_inline)) {
-    write_rows<T, TOut, GATED, decltype(act)::value>(a, acc, edges, wm * WM, wn * WN, n0 + wn * (OUT / 2), lane, mine);
+    constexpr int ACT = decltype(act)::value;
+    const int n = n0 + wn * (OUT / WGN);
+    if constexpr (Elem<T>::kInt && !GATED) {
+      if (a.R) {
+        write_rows<T, TOut, GATED, ACT, true>(a, acc, edges, wm * WM, wn * WN, n, lane, mine);
+        return;
+      }
+    }
+    write_rows<T, TOut, GATED, ACT, false>(a, acc, edges, wm * WM, wn * WN, n, lane, mine);
   });
+}
+
+// A tile a workgroup.  Of 256 rows (P = 2), those of at most 128 are done by waves
+// beside each other, in half the products.
+template <typename T, typename TOut, bool GATED, int BM, int BN, int P, bool PAST>
+__global__ __launch_bounds__(256) void tile_kernel(Args a) {
+  constexpr int STAGE = (BM + BN) * kRowBytes;
+  __shared__ int xrow[BM];
+  __shared__ Edges<BM, BN> edges;
+  const int tid = threadIdx.x;
+  const Found f = find_tile<BM, 4>(a, blockIdx.x, tid & 63);
+  if (f.group < 0) return;
+  if constexpr (BM == 256) {
+    if (f.end - f.begin <= 128) {
+      multiply_tile<T, TOut, GATED, 128, BN, P, PAST, 1, STAGE>(a, f, edges, xrow, tid);
+      return;
+    }
+  }
+  multiply_tile<T, TOut, GATED, BM, BN, P, PAST, 2, STAGE>(a, f, edges, xrow, tid);
 }
 
 // ---------------------------------------------------------------------------
 // the streaming kernel, for few rows a group
 // ---------------------------------------------------------------------------
-// BM rows and 32 rows of W by four waves that share K: wave w takes every
-// fourth piece of 128 bytes, through a ring of P slots of its own LDS, so that
-// nothing but a wave's own loads is waited for; their sums are added at the
-// end, in the waves' order.  The pieces begin apart for each workgroup: where
-// all read the same places of rows a power of two apart, the memory's channels
-// are used unevenly.  W passes the caches by where a group's rows are one tile.
-template <typename T, typename TOut, bool GATED, int BM, int P>
-__global__ __launch_bounds__(256, 2) void stream_kernel(Args a) {
+// A tile and its way to the next one: within a group the tiles of rows first,
+// then columns.
+template <int BM>
+struct Walk {
+  int group, begin, end;  // places of the group
+  int tiles, m, tn;       // tiles of its rows; this one
+  __device__ __forceinline__ void enter(const Args& a) {
+    begin = a.offsets ? clamped(a, group) : 0;
+    end = a.offsets ? clamped(a, group + 1) : a.rows;
+    tiles = (max(0, end - begin) + BM - 1) / BM;
+  }
+  // true: to other rows.  (There is a next tile, or this one stays.)
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (++m < tiles) return true;
+    m = 0;
+    if (++tn < a.tiles_n) return tiles > 1;
+    tn = 0;
+    do {
+      if (++group >= a.groups) {
+        tiles = 0;
+        group = a.groups - 1;
+        return false;
+      }
+      enter(a);
+    } while (tiles == 0);
+    return true;
+  }
+  __device__ __forceinline__ int row0() const { return begin + m * BM; }
+};
+
+// Tiles of all groups, and which one is number f of them: lane l counts those
+// of groups l * per .. + per - 1, as find_tile does.
+struct Count {
+  int g0, g1, own, incl, total;
+};
+template <int BM>
+__device__ __forceinline__ Count count_tiles(const Args& a, int lane) {
+  Count c{};
+  if (!a.offsets) {
+    c.total = (a.rows + BM - 1) / BM;
+    return c;
+  }
+  const int per = (a.groups + 63) / 64;
+  c.g0 = min(lane * per, a.groups);
+  c.g1 = min(c.g0 + per, a.groups);
+  for (int g = c.g0; g < c.g1; ++g) c.own += (max(0, clamped(a, g + 1) - clamped(a, g)) + BM - 1) / BM;
+  c.incl = wave::scan(c.own);
+  c.total = __builtin_amdgcn_readlane(c.incl, 63);
+  return c;
+}
+template <int BM>
+__device__ __forceinline__ Walk<BM> walk_from(const Args& a, const Count& c, uint32_t f) {
+  Walk<BM> w{};
+  int at = (int)f;
+  if (a.offsets) {
+    const uint32_t left = f - (uint32_t)(c.incl - c.own) * (uint32_t)a.tiles_n;
+    const uint64_t owner = __builtin_amdgcn_ballot_w64(left < (uint32_t)c.own * (uint32_t)a.tiles_n);
+    if (owner == 0) {
+      w.group = a.groups - 1;  // (offsets that do not ascend: no such tile)
+      return w;
+    }
+    int g = c.g0;
+    at = (int)left;
+    for (; g < c.g1; ++g) {
+      const int tiles = (max(0, clamped(a, g + 1) - clamped(a, g)) + BM - 1) / BM;
+      if (at < tiles * a.tiles_n) break;
+      at -= tiles * a.tiles_n;
+    }
+    const int src = __builtin_ctzll(owner);
+    w.group = __builtin_amdgcn_readlane(g, src);
+    at = __builtin_amdgcn_readlane(at, src);
+  }
+  w.enter(a);
+  w.tn = at / max(w.tiles, 1);
+  w.m = at - w.tn * w.tiles;
+  return w;
+}
+
+// Tiles of BM rows and 32 rows of W, shared out evenly over workgroups that stay:
+// one stream of loads each, which runs on from tile to tile.  The four waves
+// share K: wave w takes every fourth piece of 128 bytes, W's through a ring of P
+// slots of its own LDS and X's as operands, so that a wave waits for its own
+// loads alone; at a tile's end their sums are added in the waves' order.  The
+// pieces begin apart for each workgroup: where all read the same places of rows
+// a power of two apart, the memory's channels are used unevenly.
+template <typename T, typename TOut, bool GATED, int BM, int P, bool PAST>
+__global__ __launch_bounds__(256) void stream_kernel(Args a) {
   constexpr int BN = 32, NW = 4, TM = BM / 16, ES = sizeof(T), OUT = GATED ? 16 : 32;
   constexpr int SLOT = BN * kRowBytes;
   using Acc = typename Elem<T>::acc;
   __shared__ __attribute__((aligned(1024))) char slots[P][NW * SLOT];
+  __shared__ Acc sums[2][NW][TM * 2][64];
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Found f = find_tile<BM, 4>(a, blockIdx.x, lane);
-  if (f.group < 0) return;
+  const Count count = count_tiles<BM>(a, lane);
+  const uint32_t all = (uint32_t)count.total * (uint32_t)a.tiles_n, n = gridDim.x;
+  // consecutive shares go to one XCD
+  const uint32_t share = n % 8 == 0 ? blockIdx.x % 8 * (n / 8) + blockIdx.x / 8 : blockIdx.x;
+  const uint32_t f0 = (uint32_t)((uint64_t)all * share / n), f1 = (uint32_t)((uint64_t)all * (share + 1) / n);
+  if (f0 == f1) return;
+  Walk<BM> ahead = walk_from<BM>(a, count, f0), now = ahead;
+  if (now.tiles == 0) return;
+
   const int row_bytes = a.K * ES, KT = (row_bytes + kRowBytes - 1) / kRowBytes, pad = KT * kRowBytes - row_bytes;
   const int64_t xpitch = a.ldx * ES, wpitch = a.ldw * ES;
-  const int n0 = f.tn * OUT;
-  // (one wave's instructions: 8 rows each)
-  const RowLoader<BN, 1> lb((const char*)a.W + f.group * a.group_w * ES + n0 * wpitch,
-                            ((GATED ? 2 : 1) * (int64_t)a.N - n0) * wpitch, pad, lane,
-                            [&](int r) __attribute__((always_inline)) {
-                              const int n = column_of<GATED>(r);
-                              return n0 + n < a.N ? (n + (GATED && (r & 16) ? (int64_t)a.N : 0)) * wpitch : (int64_t)-1;
-                            });
-  // this lane's rows of X, as operands
-  const int x0 = a.gather ? 0 : f.begin;
-  const __amdgpu_buffer_rsrc_t xr = tile::make_rsrc(
-      (const char*)a.X + x0 * xpitch - pad,
-      (uint32_t)min((a.gather ? a.rows / a.per : a.rows - x0) * xpitch + pad, (int64_t)0xfffff000));
-  int entry[TM];
-  uint32_t xoff[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int at = f.begin + 16 * i + c;
-    entry[i] = at < f.end ? entry_of(a, at) : -1;
-    const int row = a.gather ? entry[i] / a.per : at;
-    // (none: past the buffer's end with a piece's second half added too)
-    xoff[i] = entry[i] < 0 ? 0xFFFFFF00u : (uint32_t)((row - x0) * xpitch) + 16 * h;
-  }
+  const int pieces = (KT + NW - 1) / NW;  // of each wave, the last perhaps none
 
-  const int n = wave < KT ? (KT - wave + NW - 1) / NW : 0;  // this wave's pieces
-  int next = n > 0 ? blockIdx.x % n : 0, left = n;
-  char* const ring = &slots[0][0];
+  // Where the loads are: a tile, and the pieces of it that are left.
+  const int wc = (lane & 7) ^ (lane >> 3);  // this lane's chunk of W's rows
+  __amdgpu_buffer_rsrc_t wr, xr;
+  uint32_t woff[4], xoff[TM];
+  int entry[TM];
+  int left = pieces, place = blockIdx.x % pieces, tiles_left = (int)(f1 - f0);
+  auto enter_rows = [&]() __attribute__((always_inline)) {
+    const int r0 = ahead.row0(), x0 = a.gather ? 0 : r0;
+    xr = tile::make_rsrc((const char*)a.X + x0 * xpitch - pad,
+                         (uint32_t)min((a.gather ? a.rows / a.per : a.rows - x0) * xpitch + pad, (int64_t)0xfffff000));
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int at = r0 + 16 * i + c;
+      entry[i] = at < ahead.end ? entry_of(a, at) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int row = a.gather ? entry[i] / a.per : r0 + 16 * i + c;
+      // (none: past the buffer's end with a piece's second half added too)
+      xoff[i] = entry[i] < 0 ? 0xFFFFFF00u : (uint32_t)((row - x0) * xpitch) + 16 * h;
+    }
+  };
+  auto enter_columns = [&]() __attribute__((always_inline)) {
+    const int n0 = ahead.tn * OUT;
+    wr = tile::make_rsrc((const char*)a.W + ahead.group * a.group_w * ES + n0 * wpitch - pad,
+                         (uint32_t)min(((GATED ? 2 : 1) * (int64_t)a.N - n0) * wpitch + pad, (int64_t)0xfffff000));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 3), k = column_of<GATED>(r);
+      woff[i] = n0 + k < a.N ? (uint32_t)((k + (GATED && (r & 16) ? (int64_t)a.N : 0)) * wpitch) + 16 * wc : 0xFFFFFFF0u;
+    }
+  };
+  enter_rows();
+  enter_columns();
   u32x4 x[P][TM][2];
   auto issue = [&](auto slot_c) __attribute__((always_inline)) {
     constexpr int J = decltype(slot_c)::value;
     // (past the last piece: zeros, no access)
-    const int kt = left <= 0 ? 0 : next * NW + wave, pad0 = left <= 0 ? 1 << 30 : kt == 0 ? pad : 0;
-    --left;
-    if (++next >= n) next = 0;
+    const bool none = place * NW + wave >= KT || tiles_left <= 0;
+    const int kt = none ? 0 : place * NW + wave, pad0 = none ? 1 << 30 : kt == 0 ? pad : 0;
 #pragma unroll
-    for (int i = 0; i < BN / 8; ++i) {
-      const uint32_t v = 16 * lb.chunk < pad0 ? 0xFFFFFFF0u : lb.voff[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(lb.rsrc, (lds_ptr)(slots[J] + wave * SLOT + i * 1024), 16, v, kt * kRowBytes, 0, 2);
-    }
+    for (int i = 0; i < BN / 8; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr)(slots[J] + wave * SLOT + i * 1024), 16,
+                                               16 * wc < pad0 ? 0xFFFFFFF0u : woff[i], kt * kRowBytes, 0, PAST ? 2 : 0);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
-        x[J][i][kk] = tile::load16(xr, 64 * kk + 16 * h < pad0 ? 0xFFFFFFF0u : xoff[i] + 64 * kk, kt * kRowBytes);
+        x[J][i][kk] = tile::load16(xr, 64 * kk + 16 * h < pad0 ? 0xFFFFFF00u : xoff[i] + 64 * kk, kt * kRowBytes);
+    if (++place == pieces) place = 0;
+    if (--left == 0) {
+      left = pieces;
+      if (--tiles_left > 0) {
+        if (ahead.next(a)) enter_rows();
+        if (ahead.tiles == 0) tiles_left = 0;
+        enter_columns();
+      }
+    }
   };
   Acc acc[TM][2] = {};
   auto multiply = [&](auto slot_c) __attribute__((always_inline)) {
@@ -563,102 +662,140 @@ __global__ __launch_bounds__(256, 2) void stream_kernel(Args a) {
         for (int i = 0; i < TM; ++i) acc[i][j] = mfma<T>(w, x[J][i][kk], acc[i][j]);
       }
   };
+  // The tile's outputs, four columns of a row a thread; alternate tiles have
+  // alternate sums, so that one barrier a tile is enough.
+  int parity = 0;
+  auto write = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sums[parity][wave][2 * i + j][lane] = acc[i][j];
+        acc[i][j] = Acc{};
+      }
+    tile::kloop_barrier<63>();  // (the loads go on)
+    constexpr int ITEMS = TM * (GATED ? 1 : 2);  // of 64 threads each
+    for (int item = wave; item < ITEMS; item += NW) {
+      const int i = GATED ? item : item >> 1, j = GATED ? 0 : item & 1;
+      const int row = now.row0() + 16 * i + c, q = row < now.end ? entry_of(a, row) : -1;
+      if (q < 0) continue;
+      const int col = now.tn * OUT + 16 * j + 4 * h;
+      const int64_t g0 = (int64_t)now.group * a.N * (GATED ? 2 : 1) + col;
+      const bool biased = has_bias(a.epi);
+      const float xs = Elem<T>::kInt ? a.xs[a.gather ? q / a.per : row] : 1.0f;
+      auto z = [&](int jj, int64_t at) __attribute__((always_inline)) {
+        Acc s = sums[parity][0][2 * i + jj][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) s += sums[parity][w][2 * i + jj][lane];
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = (float)s[e];
+          if (col + e >= a.N) continue;
+          if constexpr (Elem<T>::kInt) v[e] = v[e] * xs * a.ws[at + e];
+          if (biased) v[e] += to_f32(((const TOut*)a.bias)[at + e]);
+        }
+        return v;
+      };
+      const int to = a.scatter ? q : row;
+      f32x4 v = z(j, g0);
+      with_activation(a.epi, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = activated<decltype(act)::value>(v[e]);
+      });
+      if constexpr (GATED) v *= z(1, g0 + a.N);
+      TOut* out = (TOut*)a.C + to * a.ldc + col;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (col + e >= a.N) continue;
+        if (!GATED && a.R) v[e] += to_f32(((const TOut*)a.R)[to * a.ldr + col + e]);
+        out[e] = from_f32<TOut>(v[e]);
+      }
+    }
+    parity ^= 1;
+  };
   constexpr int OPS = BN / 8 + 2 * TM;
   static_for<P - 1>([&](auto j) __attribute__((always_inline)) { issue(j); });
-  for (int i = 0; i < n; i += P)
+  int todo = (int)(f1 - f0) * pieces, rest = pieces;
+  while (todo > 0)
     static_for<P>([&](auto j) __attribute__((always_inline)) {
-      issue(std::integral_constant<int, (decltype(j)::value + P - 1) % P>{});
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((P - 1) * OPS));
-      asm volatile("" ::: "memory");
-      multiply(j);
+      if (todo > 0) {
+        issue(std::integral_constant<int, (decltype(j)::value + P - 1) % P>{});
+        // (what else was issued meanwhile only makes the wait longer)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((P - 1) * OPS));
+        asm volatile("" ::: "memory");
+        multiply(j);
+        --todo;
+        if (--rest == 0) {
+          rest = pieces;
+          write();
+          now.next(a);
+          if (now.tiles == 0) todo = 0;
+        }
+      }
     });
-
-  // The waves' sums, four columns of a row a thread, in the ring's memory, once
-  // the zeros past the last pieces have been written there.
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-  __syncthreads();
-  Acc* const red = (Acc*)ring;
-  static_assert(NW * TM * 2 * 64 * 16 <= NW * SLOT * P, "the sums fit the ring");
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) red[(wave * TM * 2 + 2 * i + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
-  constexpr int ITEMS = TM * (GATED ? 1 : 2);  // of 64 threads each
-  if (wave >= ITEMS) return;
-  const int i = GATED ? wave : wave >> 1, j = GATED ? 0 : wave & 1;
-  const int row = f.begin + 16 * i + c, q = row < f.end ? entry_of(a, row) : -1;
-  if (q < 0) return;
-  const int col = n0 + 16 * j + 4 * h;
-  const int64_t g0 = (int64_t)f.group * a.N * (GATED ? 2 : 1) + col;
-  const bool biased = has_bias(a.epi);
-  const float xs = Elem<T>::kInt ? a.xs[a.gather ? q / a.per : row] : 1.0f;
-  auto z = [&](int jj, int64_t at) __attribute__((always_inline)) {
-    Acc s = red[(2 * i + jj) * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) s += red[(w * TM * 2 + 2 * i + jj) * 64 + lane];
-    f32x4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = (float)s[e];
-      if (col + e >= a.N) continue;
-      if constexpr (Elem<T>::kInt) v[e] = v[e] * xs * a.ws[at + e];
-      if (biased) v[e] += to_f32(((const TOut*)a.bias)[at + e]);
-    }
-    return v;
-  };
-  const int to = a.scatter ? q : row;
-  with_activation(a.epi, [&](auto act) __attribute__((always_inline)) {
-    f32x4 v = z(j, g0);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activated<decltype(act)::value>(v[e]);
-    if constexpr (GATED) v *= z(1, g0 + a.N);
-    TOut* out = (TOut*)a.C + to * a.ldc + col;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (col + e >= a.N) continue;
-      if (!GATED && a.R) v[e] += to_f32(((const TOut*)a.R)[to * a.ldr + col + e]);
-      out[e] = from_f32<TOut>(v[e]);
-    }
-  });
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // (the last pieces' zeros)
 }
 
-template <typename T, typename TOut, int BM, int BN>
+template <typename T, typename TOut, int BM, int BN, int P, bool PAST>
 hipError_t launch_tiles(Args a, bool gated, hipStream_t stream) {
   const int cols = gated ? BN / 2 : BN;
   a.tiles_n = (a.N + cols - 1) / cols;
   // tiles of rows of all groups: what their ends can add
   const int64_t tiles_m = a.offsets ? a.rows / BM + std::min(a.groups, a.rows) : (a.rows + BM - 1) / BM;
   const dim3 grid((uint32_t)(tiles_m * a.tiles_n)), block(256);
-  if (gated) hipLaunchKernelGGL((tile_kernel<T, TOut, true, BM, BN>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((tile_kernel<T, TOut, false, BM, BN>), grid, block, 0, stream, a);
+  if (gated) hipLaunchKernelGGL((tile_kernel<T, TOut, true, BM, BN, P, PAST>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((tile_kernel<T, TOut, false, BM, BN, P, PAST>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
-template <typename T, typename TOut, int BM, int P>
+// Workgroups that stay: two a CU.
+template <typename T, typename TOut, bool PAST>
 hipError_t launch_stream(Args a, bool gated, hipStream_t stream) {
+  constexpr int BM = 16, P = 4;
   const int cols = gated ? 16 : 32;
   a.tiles_n = (a.N + cols - 1) / cols;
   const int64_t tiles_m = a.offsets ? a.rows / BM + std::min(a.groups, a.rows) : (a.rows + BM - 1) / BM;
-  const dim3 grid((uint32_t)(tiles_m * a.tiles_n)), block(256);
-  if (gated) hipLaunchKernelGGL((stream_kernel<T, TOut, true, BM, P>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((stream_kernel<T, TOut, false, BM, P>), grid, block, 0, stream, a);
+  const dim3 grid((uint32_t)std::min<int64_t>(tiles_m * a.tiles_n, 512)), block(256);
+  if (gated) hipLaunchKernelGGL((stream_kernel<T, TOut, true, BM, P, PAST>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((stream_kernel<T, TOut, false, BM, P, PAST>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
+// The kernel, by what the host knows: the rows a group has on average, the bytes
+// of a row of K and those of all weights, and how many tiles there are for 256
+// CUs.  Measured (us; g: groups; W past the caches unless said):
+//   up to 4 rows a group and K of 4 KiB the streaming kernel (2 rows, 64 g, 2 x 1024
+//     of 2048, bf16: 80.3, tiles of 64 x 64 88.0; with K of 2 KiB 43.2 and 42.0);
+//   up to 48 rows tiles of 64 x 64 (32 rows, same g: 94.5, 64 x 128 102, 128 x 128
+//     122), with K below 4 KiB of 64 x 128 (i8: 24.8, 28.7, 26.4);
+//   up to 96 rows of 128 x 128 (64 rows: 126, 256 x 256 131; i8 27.9 and 29.5), beyond
+//     of 256 x 256 (128 rows: 136 and 156), where these are enough for most CUs
+//     (i8, one g, 4096 x 4096 of 4096: 53.8 us, of 128 x 128 68.3; 2048 x 4096:
+//     44.0, 35.9, with four stages, a workgroup a CU, 41.6; 1001 x 2055: 48.5, 23.8,
+//     18.2, of 64 x 64 20.1; 512 x 4096: 42.9, 23.9, 17.9, 15.4).
+// Weights of 128 MiB and more are read past the caches (64 x 64, 32 rows: 94.5 for
+// 107.7); fewer may still be in the last-level cache (i8, 16 x 8192 of 8192,
+// called in turn: 13.3, past it 14.6).
 template <typename T, typename TOut>
-hipError_t launch(Args a, bool gated, hipStream_t stream) {
-  if (a.rows <= 16 * a.groups) return launch_stream<T, TOut, 16, 4>(a, gated, stream);
-  if (a.rows <= 32 * a.groups) return launch_stream<T, TOut, 32, 4>(a, gated, stream);
-  if (a.rows >= 128 * a.groups) return launch_tiles<T, TOut, 256, 256>(a, gated, stream);
-  const int cols = gated ? 32 : 64;
-  a.tiles_n = (a.N + cols - 1) / cols;
-  const int64_t tiles_m = a.offsets ? a.rows / 64 + std::min(a.groups, a.rows) : (a.rows + 63) / 64;
-  const dim3 grid((uint32_t)(tiles_m * a.tiles_n)), block(256);
-  if (gated) hipLaunchKernelGGL((simple_kernel<T, TOut, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((simple_kernel<T, TOut, false>), grid, block, 0, stream, a);
-  return hipGetLastError();
+hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
+  const int64_t groups = std::min(a.groups, a.rows), average = (a.rows + groups - 1) / groups;
+  const int64_t cols = (int64_t)a.N * (gated ? 2 : 1), row = (int64_t)a.K * sizeof(T);
+  const bool past = groups * cols * row >= ((int64_t)128 << 20);
+  auto tiles = [&](int bm, int bn) { return groups * ((average + bm - 1) / bm) * ((cols + bn - 1) / bn); };
+  if (average <= (a.offsets ? 4 : 16) && row >= 4096)
+    return past ? launch_stream<T, TOut, true>(a, gated, stream) : launch_stream<T, TOut, false>(a, gated, stream);
+  if (average > 96 && tiles(256, 256) > 176)
+    return past ? launch_tiles<T, TOut, 256, 256, 2, true>(a, gated, stream)
+                : launch_tiles<T, TOut, 256, 256, 2, false>(a, gated, stream);
+  if (average > 48 && tiles(128, 128) > 256)
+    return past ? launch_tiles<T, TOut, 128, 128, 2, true>(a, gated, stream)
+                : launch_tiles<T, TOut, 128, 128, 2, false>(a, gated, stream);
+  if (average > 48 && tiles(128, 128) > 128) return launch_tiles<T, TOut, 128, 128, 4, false>(a, gated, stream);
+  if (past && row < 4096) return launch_tiles<T, TOut, 64, 128, 3, true>(a, gated, stream);
+  return past ? launch_tiles<T, TOut, 64, 64, 4, true>(a, gated, stream)
+              : launch_tiles<T, TOut, 64, 64, 4, false>(a, gated, stream);
 }
 
 // one translation unit per (input, output) format pair
