@@ -776,7 +776,8 @@ hipError_t launch_stream(Args a, bool gated, hipStream_t stream) {
 //     44.0, 35.9, with four stages, a workgroup a CU, 41.6; 1001 x 2055: 48.5, 23.8,
 //     18.2, of 64 x 64 20.1; 512 x 4096: 42.9, 23.9, 17.9, 15.4).
 // Weights of 128 MiB and more are read past the caches (64 x 64, 32 rows: 94.5 for
-// 107.7); fewer may still be in the last-level cache (i8, 16 x 8192 of 8192,
+// 107.7), unless a group's many rows read them often (2048 rows, 862 for 876);
+// fewer may still be in the last-level cache (i8, 16 x 8192 of 8192,
 // called in turn: 13.3, past it 14.6).
 template <typename T, typename TOut>
 hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
@@ -787,7 +788,7 @@ hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
   if (average <= (a.offsets ? 4 : 16) && row >= 4096)
     return past ? launch_stream<T, TOut, true>(a, gated, stream) : launch_stream<T, TOut, false>(a, gated, stream);
   if (average > 96 && tiles(256, 256) > 176)
-    return past ? launch_tiles<T, TOut, 256, 256, 2, true>(a, gated, stream)
+    return past && average <= 512 ? launch_tiles<T, TOut, 256, 256, 2, true>(a, gated, stream)
                 : launch_tiles<T, TOut, 256, 256, 2, false>(a, gated, stream);
   if (average > 48 && tiles(128, 128) > 256)
     return past ? launch_tiles<T, TOut, 128, 128, 2, true>(a, gated, stream)
