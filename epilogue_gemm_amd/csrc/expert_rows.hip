@@ -53,17 +53,33 @@ __device__ __forceinline__ float scale_of(float mx) {
   return mx < __builtin_inff() ? fmaxf(mx / 127.0f, 0x1p-100f) : __builtin_nanf("");
 }
 
-// Eight quotients as bytes; a scale of NaN: zeros.
+// Eight quotients as bytes; a scale of NaN: zeros.  The product with the scale's
+// reciprocal is within 128 * 3 * 2^-24 of the quotient, so that it rounds to the
+// same integer unless it lies within 2^-14 of the middle between two: the
+// quotients themselves are formed where one of a wave's does (eight divisions a
+// lane always: 57 us for 16383 x 5120).
 template <typename T, bool ANY>
-__device__ __forceinline__ void quantise8(int8_t* row, int j, int cols, u32x4 x, float s) {
+__device__ __forceinline__ void quantise8(int8_t* row, int j, int cols, u32x4 x, float s, float inv) {
   if (j >= cols) return;
-  float f[8];
+  float f[8], q[8], near = 1.0f;
   widen<T>(x, f);
-  u32x2 w = {};
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const float q = __builtin_rintf(f[u] / s);
-    w[u >> 2] |= (uint32_t)((s == s ? (int)q : 0) & 0xff) << (8 * (u & 3));
+    const float p = f[u] * inv;
+    q[u] = __builtin_rintf(p);
+    near = fminf(near, 0.5f - __builtin_fabsf(p - q[u]));
+  }
+  if (near < 0x1p-14f) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) q[u] = __builtin_rintf(f[u] / s);
+  }
+  u32x2 w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // (whole numbers of at most 128: in the lowest byte as integers)
+    const uint32_t lo = __builtin_amdgcn_perm((uint32_t)(int)q[4 * i + 1], (uint32_t)(int)q[4 * i], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm((uint32_t)(int)q[4 * i + 3], (uint32_t)(int)q[4 * i + 2], 0x04000c0cu);
+    w[i] = s == s ? lo | hi : 0u;
   }
   if (ANY && j + 8 > cols) {
     for (int u = 0; u < 8; ++u)
@@ -76,7 +92,7 @@ __device__ __forceinline__ void quantise8(int8_t* row, int j, int cols, u32x4 x,
 
 // A row in the registers of a workgroup's waves (LPR = 0), or of LPR = 16
 // lanes of one of four waves, each lane VPT pieces of eight values.
-template <typename T, bool ANY, int VPT, int LPR>
+template <typename T, bool ANY, int VPT, int LPR, bool PAST>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void quantise_rows(QuantArgs a) {
   __shared__ float part[2][16];  // of alternate rows
   constexpr int RPB = LPR ? 256 / LPR : 1;
@@ -89,7 +105,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void quantise_rows(QuantArgs a) {
     u32x4 xr[VPT];
     float mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) xr[i] = load8<ANY>(x, at + i * step, a.cols);
+    for (int i = 0; i < VPT; ++i) xr[i] = load8<ANY, PAST>(x, at + i * step, a.cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) mx = largest<T>(xr[i], mx);
     mx = LPR == 16 ? wave::over_row<MaxBits>(mx) : wave::all<MaxBits>(mx);
@@ -101,9 +117,10 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void quantise_rows(QuantArgs a) {
       for (int i = 0; i < waves; ++i) mx = MaxBits::op(mx, part[slot][i]);
     }
     const float s = scale_of(mx);
+    const float inv = 1.0f / s;
     if (at == 0) a.scale[row] = s;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) quantise8<T, ANY>(a.Y + row * a.ldy, at + i * step, a.cols, xr[i], s);
+    for (int i = 0; i < VPT; ++i) quantise8<T, ANY>(a.Y + row * a.ldy, at + i * step, a.cols, xr[i], s, inv);
   }
 }
 
@@ -120,21 +137,27 @@ __global__ __launch_bounds__(1024) void quantise_long(QuantArgs a) {
     __syncthreads();
     for (int i = 0; i < 16; ++i) mx = MaxBits::op(mx, part[i]);
     const float s = scale_of(mx);
+    const float inv = 1.0f / s;
     if (threadIdx.x == 0) a.scale[row] = s;
     for (int64_t j = threadIdx.x * 8; j < a.cols; j += 8192)
-      quantise8<T, true>(a.Y + row * a.ldy, (int)j, a.cols, load8<true>(x, (int)j, a.cols), s);
+      quantise8<T, true>(a.Y + row * a.ldy, (int)j, a.cols, load8<true>(x, (int)j, a.cols), s, inv);
     __syncthreads();  // `part` is free for the next row
   }
 }
 
 constexpr int kMaxGrid = 1 << 20;  // a grid's threads fit 32 bits; further rows by the kernels' loops
 
+// What exceeds the L2s' 32 MiB is read past the caches.
+bool past_caches(int64_t bytes) { return bytes > (int64_t)32 << 20; }
+
 template <typename T, bool ANY, int VPT, int LPR>
 hipError_t launch_quantise(const QuantArgs& a, hipStream_t stream) {
   constexpr int RPB = LPR ? 256 / (LPR + !LPR) : 1;
   const int wgs = (int)(((int64_t)a.rows + RPB - 1) / RPB);
   const int waves = LPR ? 4 : (a.cols + 512 * VPT - 1) / (512 * VPT);
-  hipLaunchKernelGGL((quantise_rows<T, ANY, VPT, LPR>), dim3(min(wgs, kMaxGrid)), dim3(64 * waves), 0, stream, a);
+  const dim3 grid(min(wgs, kMaxGrid)), block(64 * waves);
+  if (!ANY && past_caches((int64_t)a.rows * a.cols * 2)) hipLaunchKernelGGL((quantise_rows<T, ANY, VPT, LPR, !ANY>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((quantise_rows<T, ANY, VPT, LPR, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 template <typename T, bool ANY>
@@ -164,26 +187,39 @@ struct CombineArgs {
   int per, experts, cols, chunks;
 };
 
-// A workgroup a token and 2048 columns of it, eight a thread.
-template <typename T, bool ANY>
+// A workgroup a token and 2048 columns of it, eight a thread, four rows' loads and
+// the residual's at a time in flight.
+template <typename T, bool ANY, bool PAST>
 __global__ __launch_bounds__(256) void combine_rows(CombineArgs a) {
+  constexpr int B = 4;
   const int64_t units = a.tokens * a.chunks;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t t = u / a.chunks;
     const int col = (int)(u - t * a.chunks) * 2048 + threadIdx.x * 8;
-    float s[8] = {};
-    for (int j = 0; j < a.per; ++j) {
-      const int64_t q = t * a.per + j;
-      if (a.ids && (uint32_t)a.ids[q] >= (uint32_t)a.experts) continue;
-      const float w = a.weights[q];
-      float f[8];
-      widen<T>(load8<ANY>((const uint16_t*)a.Z + q * a.ldz, col, a.cols), f);
+    float s[8] = {}, f[8];
+    u32x4 r = {};
+    if (a.R) r = load8<ANY, PAST>((const uint16_t*)a.R + t * a.ldr, col, a.cols);
+    for (int j0 = 0; j0 < a.per; j0 += B) {
+      u32x4 z[B];
+      float w[B];
+      bool in[B];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(w, f[i], s[i]);
+      for (int b = 0; b < B; ++b) {
+        const int64_t q = t * a.per + min(j0 + b, a.per - 1);
+        in[b] = j0 + b < a.per && (!a.ids || (uint32_t)a.ids[q] < (uint32_t)a.experts);
+        w[b] = a.weights[q];
+        if (in[b]) z[b] = load8<ANY, PAST>((const uint16_t*)a.Z + q * a.ldz, col, a.cols);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (!in[b]) continue;
+        widen<T>(z[b], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(w[b], f[i], s[i]);
+      }
     }
     if (a.R) {
-      float f[8];
-      widen<T>(load8<ANY>((const uint16_t*)a.R + t * a.ldr, col, a.cols), f);
+      widen<T>(r, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += f[i];
     }
@@ -196,8 +232,9 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
   const int64_t lds = a.cols | a.ldz | a.ldy | (a.R ? a.ldr : 0);
   const uintptr_t ptrs = (uintptr_t)a.Z | (uintptr_t)a.R | (uintptr_t)a.Y;
   const dim3 grid((uint32_t)std::min<int64_t>(a.tokens * a.chunks, kMaxGrid));
-  if ((lds & 7) == 0 && (ptrs & 15u) == 0) hipLaunchKernelGGL((combine_rows<T, false>), grid, dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL((combine_rows<T, true>), grid, dim3(256), 0, stream, a);
+  if ((lds & 7) != 0 || (ptrs & 15u) != 0) hipLaunchKernelGGL((combine_rows<T, true, false>), grid, dim3(256), 0, stream, a);
+  else if (past_caches(a.tokens * a.per * a.cols * 2)) hipLaunchKernelGGL((combine_rows<T, false, true>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((combine_rows<T, false, false>), grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

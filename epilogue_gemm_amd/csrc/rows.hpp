@@ -10,12 +10,13 @@ namespace rows {
 // Eight consecutive values of a row, the last ones of it perhaps fewer (zeros
 // then).  ANY: rows at any address of an element (a 16-byte access off its
 // alignment is one instruction all the same) and of any length; else whole
-// and aligned.
+// and aligned.  PAST: read past the caches.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
-template <bool ANY>
+template <bool ANY, bool PAST = false>
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int j, int cols) {
   if (j >= cols) return u32x4{};
+  if constexpr (!ANY && PAST) return __builtin_nontemporal_load((const u32x4*)(row + j));
   if constexpr (!ANY) return *(const u32x4*)(row + j);
   if (j + 8 <= cols) return *(const u32x4_any*)(row + j);
   uint32_t v[8];
