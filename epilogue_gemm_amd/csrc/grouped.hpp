@@ -765,20 +765,25 @@ hipError_t launch_stream(Args a, bool gated, hipStream_t stream) {
 
 // The kernel, by what the host knows: the rows a group has on average, the bytes
 // of a row of K and those of all weights, and how many tiles there are for 256
-// CUs.  Measured (us; g: groups; W past the caches unless said):
-//   up to 4 rows a group and K of 4 KiB the streaming kernel (2 rows, 64 g, 2 x 1024
-//     of 2048, bf16: 80.3, tiles of 64 x 64 88.0; with K of 2 KiB 43.2 and 42.0);
-//   up to 48 rows tiles of 64 x 64 (32 rows, same g: 94.5, 64 x 128 102, 128 x 128
-//     122), with K below 4 KiB of 64 x 128 (i8: 24.8, 28.7, 26.4);
-//   up to 96 rows of 128 x 128 (64 rows: 126, 256 x 256 131; i8 27.9 and 29.5), beyond
-//     of 256 x 256 (128 rows: 136 and 156), where these are enough for most CUs
-//     (i8, one g, 4096 x 4096 of 4096: 53.8 us, of 128 x 128 68.3; 2048 x 4096:
-//     44.0, 35.9, with four stages, a workgroup a CU, 41.6; 1001 x 2055: 48.5, 23.8,
-//     18.2, of 64 x 64 20.1; 512 x 4096: 42.9, 23.9, 17.9, 15.4).
+// CUs.  Measured (us; W past the caches where it has 128 MiB):
+//   stream: up to 4 rows a group (16 of a single one) and K of 4 KiB.  2 rows, 64
+//     groups of 2 x 1024 x 2048 bf16 80.3, 64 x 64 88.0; K of 2 KiB 43.2 and 40.7.
+//   256 x 256: more than 96 rows, K of 2 KiB, tiles for most CUs.  i8 4096 x 4096 x
+//     4096 53.8, 128 x 128 68.3; K of 1 KiB 33.6 and 32.4; 2048 x 4096 x 4096 44.0
+//     and 35.9; 32 groups of 512 rows x 2048 x 1024 bf16 97.2 and 104; 64 rows a
+//     group 131 and 126.
+//   128 x 128, two a CU: more than 48 rows, K of 1 KiB, more than one a CU.  i8 4096
+//     x 4096 x 1024 32.4, 64 x 64 38.9; K of 256 24.7 and 24.5; 32 rows a group 122
+//     and 94.5.  Of four stages where one a CU is enough for all: 1024 x 4096 x 4096
+//     21.1, of two stages 25.2, 64 x 64 26.5; 1001 x 2055 x 4096 23.0 and (64 x 64)
+//     20.7.
+//   64 x 64: the rest, four a CU of two stages where there are many or K is short,
+//     else two of four stages.  i8 7252 x 470 x 176 7.7 and 11.0, 128 x 128 13.3; 256
+//     x 4096 x 4096 16.9 and 9.5; 32 rows a group of K of 4 KiB 121 and 94.6.
 // Weights of 128 MiB and more are read past the caches (64 x 64, 32 rows: 94.5 for
 // 107.7), unless a group's many rows read them often (2048 rows, 862 for 876);
-// fewer may still be in the last-level cache (i8, 16 x 8192 of 8192,
-// called in turn: 13.3, past it 14.6).
+// fewer may still be in the last-level cache (i8, 16 x 8192 x 8192, called in
+// turn: 13.3, past it 14.6).
 template <typename T, typename TOut>
 hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
   const int64_t groups = std::min(a.groups, a.rows), average = (a.rows + groups - 1) / groups;
@@ -787,14 +792,17 @@ hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
   auto tiles = [&](int bm, int bn) { return groups * ((average + bm - 1) / bm) * ((cols + bn - 1) / bn); };
   if (average <= (a.offsets ? 4 : 16) && row >= 4096)
     return past ? launch_stream<T, TOut, true>(a, gated, stream) : launch_stream<T, TOut, false>(a, gated, stream);
-  if (average > 96 && tiles(256, 256) > 176)
+  if (average > 96 && row >= 2048 && tiles(256, 256) > 176)
     return past && average <= 512 ? launch_tiles<T, TOut, 256, 256, 2, true>(a, gated, stream)
-                : launch_tiles<T, TOut, 256, 256, 2, false>(a, gated, stream);
-  if (average > 48 && tiles(128, 128) > 256)
+                                  : launch_tiles<T, TOut, 256, 256, 2, false>(a, gated, stream);
+  if (average > 48 && row >= 1024 && tiles(128, 128) > 256)
     return past ? launch_tiles<T, TOut, 128, 128, 2, true>(a, gated, stream)
                 : launch_tiles<T, TOut, 128, 128, 2, false>(a, gated, stream);
-  if (average > 48 && tiles(128, 128) > 128) return launch_tiles<T, TOut, 128, 128, 4, false>(a, gated, stream);
-  if (past && row < 4096) return launch_tiles<T, TOut, 64, 128, 3, true>(a, gated, stream);
+  if (average > 48 && row >= 4096 && tiles(128, 128) > 160)
+    return launch_tiles<T, TOut, 128, 128, 4, false>(a, gated, stream);
+  if (row <= 512 || (row < 4096 && tiles(64, 64) > 512))
+    return past ? launch_tiles<T, TOut, 64, 64, 2, true>(a, gated, stream)
+                : launch_tiles<T, TOut, 64, 64, 2, false>(a, gated, stream);
   return past ? launch_tiles<T, TOut, 64, 64, 4, true>(a, gated, stream)
               : launch_tiles<T, TOut, 64, 64, 4, false>(a, gated, stream);
 }
