@@ -94,7 +94,7 @@ gemm_epi_status gemm_epi_grouped_gemm(const gemm_epi_groups* groups, const void*
     return GEMM_EPI_ERR_INVALID_ARG;
   if (((uintptr_t)X | (uintptr_t)W) & 15u) return GEMM_EPI_ERR_UNSUPPORTED;
   Args a{};
-  a.offsets = g.offsets, a.order = gather || scatter ? g.order : nullptr;
+  a.offsets = g.offsets, a.order = g.order;
   a.X = X, a.W = W, a.bias = bias, a.xs = x_scale, a.ws = w_scale, a.C = C;
   a.ldx = ldx, a.ldw = K, a.ldc = ldc, a.group_w = cols * K;
   a.groups = (int)g.groups, a.rows = (int)g.rows, a.per = (int)g.per, a.N = (int)N, a.K = (int)K;

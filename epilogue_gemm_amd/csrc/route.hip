@@ -67,16 +67,13 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float logit_of(uint32_t key) {
   return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-// Of a 16-bit format the key has the expert too, a lower one above: f32's keys of
-// bf16 and f16 values end in 16 and 13 bits that are all equal, and f16 moved
-// up by three of them loses nothing.
+// Of a 16-bit format the key has the expert too, a lower one above: the order of
+// the 16-bit patterns in the upper half.
 template <typename T>
 __device__ __forceinline__ uint32_t key_of(T x, int e) {
   const uint32_t k = key_of((float)x);
   if constexpr (sizeof(T) == 4) return k;
-  else if constexpr (__is_same(T, bf16)) return k == 0 ? 0u : (k & 0xffff0000u) | (0xffffu - e);
   else {
-    // sign, 5 bits of exponent and 10 of fraction: the 16-bit pattern itself
     const uint32_t h = bits16((T)((float)x + 0.0f)), o = h & 0x8000u ? ~h & 0xffffu : h | 0x8000u;
     return k == 0 ? 0u : o << 16 | (0xffffu - e);
   }

@@ -308,6 +308,65 @@ def test_grouped_gemm_sizes(counts, N, K, dtype):
     grouped_check(counts, N, K, dtype, away=away, gather=False, out="f16" if dtype == "i8" else None)
 
 
+# One case at least for each kernel and way past the caches that the sizes
+# choose, computed in 64 bits on the GPU: rows of K in bytes, off the stages.
+KERNELS = [
+    ("stream", [1, 0, 3, 17, 2, 0, 0, 1, 4, 0, 1, 0], 130, 4112), ("stream_past", [3, 0, 1, 2] * 16, 520, 4112),
+    ("64x64_two", [40, 3, 0, 33, 65], 700, 272), ("64x64_two_past", [10, 0, 25, 4] * 16, 1040, 2064),
+    ("64x64_four", [40, 3, 0, 33, 65], 300, 2064), ("64x64_four_past", [20, 17, 0, 64, 30] * 8, 850, 4112),
+    ("128x128", [60, 130, 1, 89] * 5, 1700, 1040), ("128x128_past", [60, 130, 1, 89] * 5, 1700, 4016),
+    ("128x128_four", [1100, 300], 2300, 4112),
+    ("256x256", [1500, 700, 100, 260, 1], 2900, 2064), ("256x256_past", [300, 256, 511, 120, 129, 384, 1, 600], 4100, 4112),
+]
+
+
+@pytest.mark.parametrize("name,counts,cols,row", KERNELS, ids=[k[0] for k in KERNELS])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_gemm_every_kernel(name, counts, cols, row, dtype, gated):
+    g = torch.Generator(device="cuda").manual_seed(len(name) + row)
+    per, away = 2, 2 + sum(counts) % 2
+    out, K, N, E = "bf16" if dtype == "i8" else dtype, row // (1 if dtype == "i8" else 2), cols // (2 if gated else 1), len(counts)
+    total, cols = sum(counts) + away, N * (2 if gated else 1)
+    off, order = (t.cuda() for t in grouping(gen(row), counts, away))
+    xs = ws = None
+    if dtype == "i8":
+        x = torch.randint(-128, 128, (total // per, K), generator=g, dtype=torch.int8, device="cuda")
+        w = torch.randint(-128, 128, (E, cols, K), generator=g, dtype=torch.int8, device="cuda")
+        xs = torch.rand(total // per, generator=g, device="cuda") * 2.0 ** -7
+        ws = torch.rand(E, cols, generator=g, device="cuda") / K ** 0.5 * 2.0 ** -5
+    else:
+        x = torch.randn(total // per, K, generator=g, device="cuda").to(DT[dtype])
+        w = (torch.randn(E, cols, K, generator=g, device="cuda") * K ** -0.5).to(DT[dtype])
+    bias = torch.randn(E, cols, generator=g, device="cuda").to(DT[out])
+    epilogue = "bias_silu" if gated else "bias"
+    c, _ = blank(total, N, out)
+    gb.grouped_gemm(x, w, c, off, order, per=per, gather=True, scatter=True, gated=gated, bias=bias, epilogue=epilogue,
+                    x_scale=xs, w_scale=ws)
+    for e, n in enumerate(counts):
+        q = order[int(off[e]):int(off[e]) + n].long()
+        if not n:
+            continue
+        z, lost = pre(x[q // per], w[e], None if xs is None else xs[q // per], None if ws is None else ws[e], bias[e])
+        y, t = post(z[:, :N], lost[:, :N], epilogue, out, (z[:, N:], lost[:, N:]) if gated else None)
+        within(c[q], y.cpu(), t.cpu(), f"{name} group {e}")
+        c[q] = NAN
+    assert bool(c.isnan().all()), "rows of no entry written"
+
+
+@pytest.mark.parametrize("M,N,row", [(5, 700, 4112), (40, 700, 4112), (1500, 1800, 4112), (2300, 2100, 1040), (4100, 2900, 2064), (3000, 600, 144)])
+def test_i8_gemm_every_kernel(M, N, row):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a = torch.randint(-128, 128, (M, row), generator=g, dtype=torch.int8, device="cuda")
+    b = torch.randint(-128, 128, (N, row), generator=g, dtype=torch.int8, device="cuda")
+    xs, ws = torch.rand(M, generator=g, device="cuda") * 2.0 ** -7, torch.rand(N, generator=g, device="cuda") / row ** 0.5 * 2.0 ** -5
+    r, bias = torch.randn(M, N, generator=g, device="cuda").half(), torch.randn(N, generator=g, device="cuda").half()
+    z, lost = pre(a, b, xs, ws, bias)
+    want, tol = post(z, lost, "bias_gelu", "f16", residual=r)
+    gb.i8_gemm(a, xs, b, ws, r, bias=bias, residual=r, epilogue="bias_gelu")  # in place
+    within(r, want.cpu(), tol.cpu(), f"{M}x{N}x{row}")
+
+
 @pytest.mark.parametrize("gated,epilogue", [(g, e) for g in (False, True) for e in gb.EPILOGUES])
 def test_grouped_gemm_epilogues(gated, epilogue):
     for dtype in ("bf16", "i8"):
@@ -336,6 +395,14 @@ def test_grouped_gemm_of_any_offsets_and_order():
         either = [x[r].double() @ w[e].double().T for e in ([0] if r < 4 else [0, 2] if r < 10 else [2])]
         # (rows of two groups: each column is one of theirs)
         assert float(torch.stack([(got[r] - y).abs() for y in either]).amin(0).max()) < 0.05, r
+
+
+def test_an_order_counts_where_nothing_is_gathered_or_scattered():
+    x, w = rand(gen(1), 8, 64, dtype="bf16"), rand(gen(2), 1, 16, 64, dtype="bf16")
+    order = torch.tensor([3, -1, 0, 8, 5, 6, 7, 1], dtype=torch.int32)
+    c, _ = blank(8, 16, "bf16")
+    gb.grouped_gemm(x.cuda(), w.cuda(), c, torch.tensor([0, 7], dtype=torch.int32).cuda(), order.cuda())
+    assert c.cpu().isnan().all(1).tolist() == [False, True, False, True, False, False, False, True]
 
 
 def test_products_keep_no_infinities_from_rows_that_are_none():
