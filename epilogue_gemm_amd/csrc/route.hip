@@ -1,6 +1,9 @@
 // route.hip -- the router of a layer of experts: the k largest logits of each
 // token and their weights, and the entries (token, choice) in the stable order
-// of their experts.
+// of their experts.  A choice is a largest key over lanes and its removal; bound by
+// these instructions for many tokens (16384 tokens, 8 of 256: bf16 6.9 us, f32 8.3;
+// 64 lanes a token 12.4 and 14.6), by launches and latencies for few (32 tokens, 8
+// of 128, with the order 4.7 us in one kernel, in two 7).
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -192,29 +195,26 @@ struct GroupArgs {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef i32x4 i32x4_any __attribute__((aligned(4)));
 
-// A workgroup a group (the last one: the entries of none).  Each reads all ids to
-// count those of lower groups, in rounds of a batch of 2048 consecutive ones a
-// wave, a lane four of each 256 (waves far apart would meet in the same channels
-// of the L2: 131072 of 256 groups 28.8 us), and keeps a bit for each of its own
-// (KEPT: up to 131072 entries, else it reads them again); then it writes these
-// in their order, round by round.
+// A workgroup a group.  Each reads all ids to count those of lower groups, in
+// rounds of a batch of 2048 consecutive ones a wave, a lane four of each 256, and
+// keeps a bit for each of its own (KEPT: up to 131072 entries, else it reads them
+// again); then it writes these in their order.  Bound by the comparisons, five
+// instructions for each id and group (131072 ids of 256 groups 11.2 us; with a
+// scan over lanes for each 256 ids 20.7).
 constexpr int kKept = 131072;
 template <bool KEPT>
 __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
-  __shared__ int below[16], own[2][16];
+  __shared__ int below[16], own[4][16];
   const int g = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int rounds = (int)(((int64_t)a.rows + 32767) / 32768);
-  const bool rest = g == a.groups;
   // Four of this lane's ids: those of lower groups (an id of none is above all
-  // groups as an unsigned number), and a bit for each of its own, from g on one
-  // number or all that there are, the first one the highest: a comparison and an
-  // addition with carry each.
-  const uint32_t width = rest ? 0u - (uint32_t)g : 1u;
+  // groups as an unsigned number), and a bit for each of its own, the first one
+  // the highest: a comparison and an addition with carry each.
   auto four = [&](const i32x4& x, uint32_t& bits, uint32_t& lower) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       lower += (uint32_t)x[u] < (uint32_t)g;
-      bits = bits + bits + ((uint32_t)x[u] - (uint32_t)g < width);
+      bits = bits + bits + (x[u] == g);
     }
   };
   uint32_t lower = 0;
@@ -231,20 +231,43 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) four(x[j], bits, lower);
     } else {
-      uint32_t there = 0;  // the bits of ids before the end
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool in = i0 + 256 * j + 4 * lane + u < a.rows;
-          x[j][u] = in ? p[256 * j + u] : -1;
-          there = there + there + in;
-        }
+        for (int u = 0; u < 4; ++u) x[j][u] = i0 + 256 * j + 4 * lane + u < a.rows ? p[256 * j + u] : -1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) four(x[j], bits, lower);
-      bits &= there;
     }
     return bits;
+  };
+  // this wave's own ones of a batch, from place `to` on: each block's counts in
+  // 16 bits of four words, summed over lower lanes and lower blocks, are the
+  // places, of which a lane takes one after the other
+  auto write = [&](int round, uint32_t bits, int to) __attribute__((always_inline)) {
+    uint32_t place[4];
+    int before = to;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __builtin_popcount(bits >> (28 - 8 * i) & 15u), hi = __builtin_popcount(bits >> (24 - 8 * i) & 15u);
+      const uint32_t n = lo | hi << 16, upto = (uint32_t)wave::scan((int)n), sum = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+      const int mid = before - to + (int)(sum & 0xffffu);
+      place[i] = upto - n + ((uint32_t)(before - to) | (uint32_t)mid << 16);
+      before = to + mid + (int)(sum >> 16);
+    }
+    const int first = round * 32768 + 2048 * wave + 4 * lane;
+    while (__builtin_amdgcn_ballot_w64(bits != 0)) {
+      if (bits != 0) {
+        const int b = __builtin_clz(bits), j = b >> 2, half = (j & 1) * 16;
+        uint32_t p = place[0];
+        p = j >> 1 == 1 ? place[1] : p;
+        p = j >> 1 == 2 ? place[2] : p;
+        p = j >> 1 == 3 ? place[3] : p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) place[i] += j >> 1 == i ? 1u << half : 0u;
+        a.order[to + (int)(p >> half & 0xffffu)] = first + 256 * j + (b & 3);
+        bits &= ~(0x80000000u >> b);
+      }
+    }
   };
   uint32_t kept[4] = {};
   if constexpr (KEPT) {
@@ -256,41 +279,42 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
   }
   const int lower_sum = wave::scan((int)lower);
   if (lane == 63) below[wave] = lower_sum;
+  if constexpr (KEPT) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = wave::scan(__builtin_popcount(kept[k]));
+      if (lane == 63) own[k][wave] = n;
+    }
+  }
   __syncthreads();
   int at = 0;
   for (int i = 0; i < 16; ++i) at += below[i];
   if (threadIdx.x == 0) a.offsets[g] = at;
-  // a round's own ones, from `at` on (a wave a round ahead writes the other half)
-  auto write = [&](int round, uint32_t bits) __attribute__((always_inline)) {
-    const int incl = wave::scan(__builtin_popcount(bits));
-    if (lane == 63) own[round & 1][wave] = incl;
-    __syncthreads();
-    int before = at, mine = 0;
-    for (int i = 0; i < 16; ++i) {
-      const int n = own[round & 1][i];
-      before += i < wave ? n : 0;
-      mine = i == wave ? n : mine;
-      at += n;
-    }
-    if (mine == 0) return;
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t own4 = bits >> (28 - 4 * j) & 15u;
-      if (__builtin_amdgcn_ballot_w64(own4 != 0) == 0) continue;
-      const int n = __builtin_popcount(own4), upto = wave::scan(n);
-      int to = before + upto - n;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (own4 >> (3 - u) & 1u)
-          a.order[to++] = rest ? -1 : (int)((int64_t)round * 32768 + 2048 * wave + 256 * j + 4 * lane + u);
-      before += __builtin_amdgcn_readlane(upto, 63);
-    }
-  };
   if constexpr (KEPT) {
+    const int n = (&own[0][0])[lane], upto = at + wave::scan(n);
+    at = __builtin_amdgcn_readlane(upto, 63);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k < rounds) write(k, kept[k]);
+      if (k < rounds) write(k, kept[k], __builtin_amdgcn_readlane(upto - n, 16 * k + wave));
   } else {
-    for (int k = 0; k < rounds; ++k) write(k, batch(k));
+    for (int k = 0; k < rounds; ++k) {
+      // (a wave a round ahead writes the other half)
+      const uint32_t bits = batch(k);
+      const int n = wave::scan(__builtin_popcount(bits));
+      if (lane == 63) own[k & 1][wave] = n;
+      __syncthreads();
+      int to = at;
+      for (int i = 0; i < 16; ++i) {
+        to += i < wave ? own[k & 1][i] : 0;
+        at += own[k & 1][i];
+      }
+      write(k, bits, to);
+    }
+  }
+  // the last group's workgroup knows where the order ends
+  if (g == a.groups - 1) {
+    if (threadIdx.x == 0) a.offsets[a.groups] = at;
+    for (int64_t i = at + (int64_t)threadIdx.x; i < a.rows; i += 1024) a.order[i] = -1;
   }
 }
 
@@ -332,8 +356,8 @@ __global__ __launch_bounds__(1024) void route_few(Args a, GroupArgs b) {
 }
 
 hipError_t launch_group(const GroupArgs& a, hipStream_t stream) {
-  if (a.rows <= kKept) hipLaunchKernelGGL(group_kernel<true>, dim3(a.groups + 1), dim3(1024), 0, stream, a);
-  else hipLaunchKernelGGL(group_kernel<false>, dim3(a.groups + 1), dim3(1024), 0, stream, a);
+  if (a.rows <= kKept) hipLaunchKernelGGL(group_kernel<true>, dim3(a.groups), dim3(1024), 0, stream, a);
+  else hipLaunchKernelGGL(group_kernel<false>, dim3(a.groups), dim3(1024), 0, stream, a);
   return hipGetLastError();
 }
 
