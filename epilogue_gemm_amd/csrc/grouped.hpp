@@ -3,7 +3,24 @@
 //     C[.] = act(X[.] W[g]^T + bias[g])   or   act(gate) * up
 //
 // for 16-bit formats and, with scales, 8-bit integers; one group of all rows
-// is the 8-bit product.
+// is the 8-bit product.  Two kernels on v_mfma_f32_16x16x32 and its 8-bit like
+// v_mfma_i32_16x16x64_i8, whose operands are the same 16 bytes a lane, so that one
+// layout in LDS serves both:
+//   * tile_kernel: tiles of 64 x 64 to 256 x 256, rows of X gathered by the direct
+//     copies themselves, the group found by each workgroup from the offsets.  Large
+//     ones are bound by the power limit (i8 8192^3 398 to 420 us, 2.6 to 2.8 POP/s
+//     at some 1.95 GHz with the matrix units 67 % busy; bf16, 8 groups of 16384
+//     rows, 2 x 4096 of 4096, 862 us, 1.28 PFLOP/s), those of short K by the
+//     epilogue and the lookups (32 groups of 12284 rows, 4096 of 2048, i8: 160 us,
+//     of which the matrix units are busy 41 %), small ones by the latency of a
+//     k-step;
+//   * stream_kernel: for few rows a group, bound by W from HBM (32 tokens, 4 of 64,
+//     2 x 1024 of 2048, bf16: 80.5 us, 5.9 TB/s, 1.00 x the least bytes).
+// Measured and not kept: a workgroup a tile of the streaming kernel (83.9 us for
+// 80.5), twice its ring with one workgroup a CU (82.8), 32 or 64 rows a tile there
+// (X as operands for rows that mostly are none: 88.7, 105); 128 x 256 tiles of three
+// stages (531 us for 398 at 8192^3); 64 x 64 with eight stages, a workgroup a CU
+// (the same for few tiles, 65 us for 52 at 2048 x 4096 x 4096).
 #pragma once
 
 #include <algorithm>

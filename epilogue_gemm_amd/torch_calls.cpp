@@ -1,7 +1,7 @@
 // torch_calls.cpp -- the tensor calls of binding.py for the operators of a
-// decode step and of a layer of experts: checks of the arguments and the C call, for loops whose time is
-// the host's (a 4 x 4096 rmsnorm takes the host 4.0 us, in Python over ctypes
-// 6.7).  torch is used for what a tensor is -- device, format, shape,
+// decode step and of a layer of experts: checks of the arguments and the C call,
+// for loops whose time is the host's (a 4 x 4096 rmsnorm takes the host 4.0 us,
+// in Python over ctypes 6.7).  torch is used for what a tensor is -- device, format, shape,
 // strides and address -- and for nothing else.
 //
 // Every function takes the current device's index and the stream, then the

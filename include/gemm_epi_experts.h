@@ -146,9 +146,10 @@ typedef struct gemm_epi_groups {
  * without order, rows not a multiple of per with GATHER, a pointer off its
  * element's alignment), UNSUPPORTED (rows of K not a multiple of 16 bytes, K >=
  * 2^17, X or W not 16-byte aligned, ldx not a multiple of 16 bytes or above 16
- * MiB, more than 1024 groups, any size or leading dimension >= 2^31, X of 4 GiB less 64 KiB or
- * more with GATHER, gates of a group of more than 2 GiB, more than 2^25 blocks of 16 x 16 products, counting one more
- * for each group), HIP. */
+ * MiB, more than 1024 groups, any size or leading dimension >= 2^31, X of 4 GiB
+ * less 64 KiB or more with GATHER, gates of a group of more than 2 GiB, more
+ * than 2^25 blocks of 16 x 16 products, counting one more for each group),
+ * HIP. */
 gemm_epi_status gemm_epi_grouped_gemm(const gemm_epi_groups* groups, const void* X, int64_t ldx, const float* x_scale,
                                       const void* W, const float* w_scale, const void* bias, void* C, int64_t ldc,
                                       int64_t N, int64_t K, int flags, gemm_epi_epilogue epilogue,
