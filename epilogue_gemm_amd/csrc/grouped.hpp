@@ -794,8 +794,9 @@ hipError_t launch_stream(Args a, bool gated, hipStream_t stream) {
 //     and 94.5.  Of four stages where one a CU is enough for all: 1024 x 4096 x 4096
 //     21.1, of two stages 25.2, 64 x 64 26.5; 1001 x 2055 x 4096 23.0 and (64 x 64)
 //     20.7.
-//   64 x 64: the rest, four a CU of two stages where there are many or K is short,
-//     else two of four stages.  i8 7252 x 470 x 176 7.7 and 11.0, 128 x 128 13.3; 256
+//   64 x 64: the rest, four a CU of two stages where there are many (and K below 4
+//     KiB, or more than 48 rows) or K is short, else two of four stages.  i8 1001 x
+//     2055 x 4096 20.7 and 22.3; 7252 x 470 x 176 7.7 and 11.0, 128 x 128 13.3; 256
 //     x 4096 x 4096 16.9 and 9.5; 32 rows a group of K of 4 KiB 121 and 94.6.
 // Weights of 128 MiB and more are read past the caches (64 x 64, 32 rows: 94.5 for
 // 107.7), unless a group's many rows read them often (2048 rows, 862 for 876);
@@ -817,7 +818,7 @@ hipError_t launch(const Args& a, bool gated, hipStream_t stream) {
                 : launch_tiles<T, TOut, 128, 128, 2, false>(a, gated, stream);
   if (average > 48 && row >= 4096 && tiles(128, 128) > 160)
     return launch_tiles<T, TOut, 128, 128, 4, false>(a, gated, stream);
-  if (row <= 512 || (row < 4096 && tiles(64, 64) > 512))
+  if (row <= 512 || (tiles(64, 64) > 512 && (row < 4096 || average > 48)))
     return past ? launch_tiles<T, TOut, 64, 64, 2, true>(a, gated, stream)
                 : launch_tiles<T, TOut, 64, 64, 2, false>(a, gated, stream);
   return past ? launch_tiles<T, TOut, 64, 64, 4, true>(a, gated, stream)

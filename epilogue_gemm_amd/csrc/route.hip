@@ -384,7 +384,8 @@ hipError_t launch_route(const Args& a, const GroupArgs* b, hipStream_t stream) {
   }
   hipError_t e;
   if (a.experts > 512) e = launch_tokens<T, 16, 64>(a, stream);
-  else if (a.experts > 256) e = launch_tokens<T, 8, 64>(a, stream);
+  else if (a.experts > 384) e = launch_tokens<T, 32, 16>(a, stream);
+  else if (a.experts > 256) e = launch_tokens<T, 24, 16>(a, stream);
   else if (a.experts > 128) e = launch_tokens<T, 16, 16>(a, stream);
   else if (a.experts > 64) e = launch_tokens<T, 8, 16>(a, stream);
   else if (a.experts > 16) e = launch_tokens<T, 4, 16>(a, stream);

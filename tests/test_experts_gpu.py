@@ -499,7 +499,7 @@ def route_check(logits, per, score, renormalise, scale=1.0, extra=0):
 
 
 @pytest.mark.parametrize("tokens,experts,per", [(1, 1, 1), (1, 8, 2), (5, 4, 4), (3, 64, 6), (33, 60, 4), (2, 65, 8), (32, 128, 8),
-                                                (70, 129, 7), (9, 256, 8), (300, 160, 6), (4, 384, 8), (7, 1024, 64),
+                                                (70, 129, 7), (9, 256, 8), (300, 160, 6), (4, 384, 8), (7, 1024, 64), (130, 512, 8), (9, 300, 6), (3, 600, 20),
                                                 (2000, 16, 2), (5, 100, 64), (1030, 256, 8), (3000, 8, 2)])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("score,renormalise", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
@@ -723,6 +723,24 @@ def test_other_stream_and_order_of_work():
         layer.run()
     s.synchronize()
     assert torch.equal(layer.o, want)
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams without an order between them, on inputs
+    of their own: each gives the bits that it gives alone."""
+    layers = [Layer(700, 12, 3, 512, 384, "i8", 7), Layer(800, 16, 4, 512, 256, "bf16", 8)]
+    for i, layer in enumerate(layers):
+        layer.x.copy_(rand(gen(i), layer.tokens, 512, dtype="bf16"))
+        layer.run()
+    want = [(layer.o.clone(), layer.order.clone(), layer.w.clone()) for layer in layers]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for layer, stream in zip(layers, streams):
+            layer.run(stream=stream)
+    torch.cuda.synchronize()
+    for layer, (o, order, w) in zip(layers, want):
+        assert torch.equal(layer.o, o) and torch.equal(layer.order, order) and torch.equal(layer.w, w)
 
 
 # ---- refusals of the tensor calls ------------------------------------------------------
