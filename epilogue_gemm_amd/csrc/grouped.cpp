@@ -82,11 +82,13 @@ gemm_epi_status gemm_epi_grouped_gemm(const gemm_epi_groups* groups, const void*
   if ((((uintptr_t)g.offsets | (uintptr_t)g.order | (uintptr_t)x_scale | (uintptr_t)w_scale) & 3u) ||
       ((uintptr_t)C & 1u) || (biased(epilogue) && ((uintptr_t)bias & 1u)))
     return GEMM_EPI_ERR_INVALID_ARG;
-  for (const int64_t n : {g.rows, g.per, N, ldc})
+  // (each bounded by itself before a product of it is formed)
+  for (const int64_t n : {g.rows, g.per, N, ldx, ldc})
     if (n >= kLim) return GEMM_EPI_ERR_UNSUPPORTED;
-  const int64_t size = i8 ? 1 : 2, cols = gated ? 2 * N : N;
-  if ((gated && N * K * size > kMaxGate) || K * size % 16 != 0 || K >= (1 << 17) || ldx * size % 16 != 0 || ldx * size > kMaxPitch || g.groups > 1024 || cols >= kLim ||
-      too_many(g.rows, g.groups, cols) || (gather && g.rows / g.per * ldx * size >= (int64_t)0xffff0000))
+  if (K >= (1 << 17) || g.groups > 1024) return GEMM_EPI_ERR_UNSUPPORTED;
+  const int64_t size = i8 ? 1 : 2, cols = gated ? 2 * N : N, pitch = ldx * size;
+  if ((gated && N * K * size > kMaxGate) || K * size % 16 != 0 || pitch % 16 != 0 || pitch > kMaxPitch || cols >= kLim ||
+      too_many(g.rows, g.groups, cols) || (gather && g.rows / g.per * pitch >= (int64_t)0xffff0000))
     return GEMM_EPI_ERR_UNSUPPORTED;
   if (g.rows == 0) return GEMM_EPI_OK;
   if (!g.offsets || ((gather || scatter) && !g.order) || !X || !W || !C || i8 != (x_scale != nullptr) ||

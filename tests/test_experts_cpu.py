@@ -149,6 +149,17 @@ def test_grouped_gemm_refusals(places, kw, want):
     assert _grouped(places, **kw) == want
 
 
+@pytest.mark.parametrize("kw", [
+    {"ldx": 1 << 62}, {"ldx": (1 << 62) + 8}, {"ldx": (1 << 63) - 8}, {"ldx": 1 << 31}, {"ldx": 1 << 61, "dtype": "f16", "out_dtype": "f16"},
+    {**_I8, "ldx": 1 << 62}, {**_I8, "ldx": (1 << 63) - 16}, {"K": 1 << 62, "ldx": 1 << 62}, {"K": (1 << 63) - 8, "ldx": (1 << 63) - 1},
+    {**_I8, "K": 1 << 62, "ldx": 1 << 62}, {"N": (1 << 62) + 8, "ldc": 1 << 62 | 16},
+])
+@pytest.mark.parametrize("flags", [0, gb.GATHER, gb.GATED, gb.GATHER | gb.GATED])
+def test_grouped_gemm_refuses_sizes_whose_bytes_pass_64_bits(kw, flags):
+    """Sizes and distances near 2^63: their bytes are no number of 64 bits."""
+    assert _grouped(**{"flags": flags, **kw}) == UNSUPPORTED
+
+
 def _combine(**kw):
     a = dict(Z=P, ldz=64, weights=P, ids=P, experts=4, R=P, ldr=64, Y=P, ldy=64, tokens=0, per=4, cols=64, dtype="bf16",
              stream=None)
