@@ -129,6 +129,24 @@ def test_quantise_special_rows(cols):
     assert scale[1:4].isnan().all() and scale[0] == 2.0 ** -100 and not y[0].any()
 
 
+# Aligned rows of more than 32 MiB in each of the row kernels (16 lanes a row,
+# one to four pieces a thread), and more rows than the 2^20 workgroups of a grid
+# take at once.
+@pytest.mark.parametrize("rows,cols", [(140000, 128), (35000, 512), (4200, 4096), (1030, 16384), (520, 32768),
+                                       ((1 << 20) + 77, 136), ((1 << 20) + 3, 1032), ((1 << 20) + 5, 131), ((1 << 24) + 5, 8)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_quantise_many_rows(rows, cols, dtype):
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.empty(rows, cols, dtype=DT[dtype], device="cuda").normal_(generator=g)
+    x[torch.tensor([1, rows // 2, rows - 2]), torch.tensor([0, cols // 2, cols - 1])] = torch.tensor([INF, NAN, -INF], dtype=DT[dtype], device="cuda")
+    y, s = torch.full((rows, cols), 99, dtype=torch.int8, device="cuda"), torch.full((rows,), -1.0, device="cuda")
+    gb.quantise_i8(x, y, s)
+    step = max(1, (1 << 27) // cols)
+    for i in range(0, rows, step):
+        q, sw = quantised(x[i:i + step])
+        assert torch.equal(y[i:i + step], q) and same_scale(s[i:i + step], sw.cpu()), i
+
+
 # ---- products -------------------------------------------------------------------
 
 def act(z, epilogue):
@@ -557,6 +575,25 @@ def test_group_rows(rows, groups):
     assert torch.equal(off.cpu(), torch.searchsorted(key, torch.arange(groups + 1, dtype=torch.int32)).int())
 
 
+# Ids beside the most of which a lane keeps its own (131072), partial and odd
+# rounds of 32768 among them.
+@pytest.mark.parametrize("rows,groups", [(98305, 33), (131071, 5), (131072, 256), (131073, 60), (163878, 1024), (196608, 3), (229377, 64), (400000, 16)])
+def test_group_rows_of_many_ids(rows, groups):
+    test_group_rows(rows, groups)
+    # nearly all in one group, then all in it
+    for others in (0.01, 0.0):
+        for most in (0, groups - 1):
+            g = gen(rows + most)
+            ids = torch.where(torch.rand(rows, generator=g) < others, torch.randint(-1, groups, (rows,), generator=g), most).int()
+            off = torch.full((groups + 2,), 9, dtype=torch.int32, device="cuda")
+            order = torch.full((rows + 1,), 9, dtype=torch.int32, device="cuda")
+            gb.group_rows(ids.cuda(), off[:-1], order[:-1])
+            key, want = torch.where(ids >= 0, ids, groups).sort(stable=True)
+            assert torch.equal(order[:-1].cpu(), torch.where(key < groups, want, -1).int()), (others, most)
+            assert torch.equal(off[:-1].cpu(), torch.searchsorted(key, torch.arange(groups + 1, dtype=torch.int32)).int())
+            assert int(off[-1]) == 9 == int(order[-1]), "written past the end"
+
+
 def test_route_without_tokens():
     off = torch.full((9,), 7, dtype=torch.int32, device="cuda")
     empty = torch.empty(0, 2, device="cuda")
@@ -588,6 +625,27 @@ def test_combine(tokens, per, cols, dtype):
         gb.combine(strided(zz, extra), ww.cuda(), ids.cuda() if masked else None, y, experts=3, residual=strided(r, 2 * extra) if res else None)
         within(y, want, lost * (1 + e) + e * want.abs() + SUB[dtype], f"{tokens}x{per}x{cols} extra {extra}")
         assert bool(buf[:, cols:].isnan().all()), "written past the rows"
+
+
+# Aligned rows of more than 32 MiB, and more tokens than the 2^20 workgroups of a
+# grid take at once.
+@pytest.mark.parametrize("tokens,per,cols", [(1100, 4, 4096), (2050, 3, 2880), ((1 << 20) + 9, 2, 16), ((1 << 20) + 9, 2, 15)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_combine_many_rows(tokens, per, cols, dtype):
+    g = torch.Generator(device="cuda").manual_seed(tokens + cols)
+    z, r = (torch.empty(n, cols, dtype=DT[dtype], device="cuda").normal_(generator=g) for n in (tokens * per, tokens))
+    w = torch.rand(tokens, per, generator=g, device="cuda")
+    ids = torch.randint(-1, 4, (tokens, per), generator=g, dtype=torch.int32, device="cuda")
+    there = (ids >= 0) & (ids < 3)
+    z[~there.reshape(-1)] = NAN
+    terms = torch.where(there[..., None], w.double()[..., None] * z.double().view(tokens, per, cols), 0.0)
+    e = torch.finfo(DT[dtype]).eps / 2
+    for res in (False, True):  # (in place the second time)
+        want = terms.sum(1) + (r.double() if res else 0.0)
+        lost = (per + 1) * U * (terms.abs().sum(1) + want.abs())
+        y = r if res else torch.full_like(r, NAN)
+        gb.combine(z, w, ids, y, experts=3, residual=r if res else None)
+        within(y, want.cpu(), (lost * (1 + e) + e * want.abs() + SUB[dtype]).cpu(), f"{tokens}x{per}x{cols} residual {res}")
 
 
 def test_combine_in_place():
