@@ -75,8 +75,26 @@ struct Found {
   int tn;
 };
 
-// Places of group g, of offsets that may hold anything.
+// Offset g, of those that may hold anything.
 __device__ __forceinline__ int clamped(const Args& a, int g) { return max(0, min(a.offsets[g], a.rows)); }
+
+// Offsets that descend somewhere count as no lower than any before them, so that
+// no place is of two groups and a grid for ascending ones holds all tiles.  The
+// group that has tile f (-1: none) and its places [begin, end), by a walk from the
+// first group on; f is then the tile's number in the group, of `tiles` of rows.
+template <int BM>
+__device__ __forceinline__ int walk_raised(const Args& a, uint32_t& f, int& begin, int& end, int& tiles) {
+  end = clamped(a, 0);
+  for (int g = 0; g < a.groups; ++g) {
+    begin = end;
+    end = max(begin, clamped(a, g + 1));
+    tiles = (end - begin + BM - 1) / BM;
+    const uint32_t all = (uint32_t)tiles * (uint32_t)a.tiles_n;
+    if (f < all) return g;
+    f -= all;
+  }
+  return -1;
+}
 
 // A tile of those of all groups, from the workgroup's number.  Workgroups go to
 // the 8 XCDs in turn: consecutive tiles go to one XCD, group by group, in each
@@ -87,23 +105,33 @@ __device__ __forceinline__ int clamped(const Args& a, int g) { return max(0, min
 template <int BM, int PANEL>
 __device__ __forceinline__ Found find_tile(const Args& a, int id, int lane) {
   int own = 0, g0 = 0, g1 = 0, incl = 0, total;
+  bool descends = false;
   if (a.offsets) {
     const int per = (a.groups + 63) / 64;
     g0 = min(lane * per, a.groups);
     g1 = min(g0 + per, a.groups);
-    for (int g = g0; g < g1; ++g) own += (max(0, clamped(a, g + 1) - clamped(a, g)) + BM - 1) / BM;
-    // (offsets that do not ascend may count rows twice: the sum over lanes then
-    // wraps, a lane's own does not)
+    int signs = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int n = clamped(a, g + 1) - clamped(a, g);
+      own += (max(0, n) + BM - 1) / BM;
+      signs |= n;
+    }
+    descends = __builtin_amdgcn_ballot_w64(signs < 0) != 0;
     incl = wave::scan(own);
     total = __builtin_amdgcn_readlane(incl, 63);
   } else {
     total = (a.rows + BM - 1) / BM;
   }
   const uint32_t all = (uint32_t)total * (uint32_t)a.tiles_n;
-  if ((uint32_t)id >= all) return Found{-1, 0, 0, 0};
+  if (!descends && (uint32_t)id >= all) return Found{-1, 0, 0, 0};
   const uint32_t x = id & 7, f = x * (all >> 3) + min(x, all & 7) + ((uint32_t)id >> 3);
   int g = 0, begin = 0, end = a.rows, tiles = total, at = (int)f;
-  if (a.offsets) {
+  if (__builtin_expect(descends, 0)) {
+    uint32_t left = (uint32_t)id;
+    g = walk_raised<BM>(a, left, begin, end, tiles);
+    if (g < 0) return Found{-1, 0, 0, 0};
+    at = (int)left;
+  } else if (a.offsets) {
     const uint32_t left = f - (uint32_t)(incl - own) * (uint32_t)a.tiles_n;
     const uint64_t owner = __builtin_amdgcn_ballot_w64(left < (uint32_t)own * (uint32_t)a.tiles_n);
     if (owner == 0) return Found{-1, 0, 0, 0};
@@ -508,10 +536,11 @@ template <int BM>
 struct Walk {
   int group, begin, end;  // places of the group
   int tiles, m, tn;       // tiles of its rows; this one
+  // `group`, the one before it ending at `end`
   __device__ __forceinline__ void enter(const Args& a) {
-    begin = a.offsets ? clamped(a, group) : 0;
-    end = a.offsets ? clamped(a, group + 1) : a.rows;
-    tiles = (max(0, end - begin) + BM - 1) / BM;
+    begin = end;
+    end = a.offsets ? max(begin, clamped(a, group + 1)) : a.rows;
+    tiles = (end - begin + BM - 1) / BM;
   }
   // true: to other rows.  (There is a next tile, or this one stays.)
   __device__ __forceinline__ bool next(const Args& a) {
@@ -536,6 +565,7 @@ struct Walk {
 // of groups l * per .. + per - 1, as find_tile does.
 struct Count {
   int g0, g1, own, incl, total;
+  bool descends;
 };
 template <int BM>
 __device__ __forceinline__ Count count_tiles(const Args& a, int lane) {
@@ -547,7 +577,21 @@ __device__ __forceinline__ Count count_tiles(const Args& a, int lane) {
   const int per = (a.groups + 63) / 64;
   c.g0 = min(lane * per, a.groups);
   c.g1 = min(c.g0 + per, a.groups);
-  for (int g = c.g0; g < c.g1; ++g) c.own += (max(0, clamped(a, g + 1) - clamped(a, g)) + BM - 1) / BM;
+  int signs = 0;
+  for (int g = c.g0; g < c.g1; ++g) {
+    const int n = clamped(a, g + 1) - clamped(a, g);
+    c.own += (max(0, n) + BM - 1) / BM;
+    signs |= n;
+  }
+  c.descends = __builtin_amdgcn_ballot_w64(signs < 0) != 0;
+  if (__builtin_expect(c.descends, 0)) {
+    // (no tile has this number: the walk takes from it all that there are)
+    uint32_t f = ~0u;
+    int begin, end, tiles;
+    walk_raised<BM>(a, f, begin, end, tiles);
+    c.total = (int)(~f / (uint32_t)a.tiles_n);
+    return c;
+  }
   c.incl = wave::scan(c.own);
   c.total = __builtin_amdgcn_readlane(c.incl, 63);
   return c;
@@ -556,13 +600,15 @@ template <int BM>
 __device__ __forceinline__ Walk<BM> walk_from(const Args& a, const Count& c, uint32_t f) {
   Walk<BM> w{};
   int at = (int)f;
+  if (__builtin_expect(c.descends, 0)) {
+    w.group = walk_raised<BM>(a, f, w.begin, w.end, w.tiles);
+    w.tn = (int)f / w.tiles;
+    w.m = (int)f - w.tn * w.tiles;
+    return w;
+  }
   if (a.offsets) {
     const uint32_t left = f - (uint32_t)(c.incl - c.own) * (uint32_t)a.tiles_n;
     const uint64_t owner = __builtin_amdgcn_ballot_w64(left < (uint32_t)c.own * (uint32_t)a.tiles_n);
-    if (owner == 0) {
-      w.group = a.groups - 1;  // (offsets that do not ascend: no such tile)
-      return w;
-    }
     int g = c.g0;
     at = (int)left;
     for (; g < c.g1; ++g) {
@@ -573,9 +619,10 @@ __device__ __forceinline__ Walk<BM> walk_from(const Args& a, const Count& c, uin
     const int src = __builtin_ctzll(owner);
     w.group = __builtin_amdgcn_readlane(g, src);
     at = __builtin_amdgcn_readlane(at, src);
+    w.end = clamped(a, w.group);
   }
   w.enter(a);
-  w.tn = at / max(w.tiles, 1);
+  w.tn = at / w.tiles;
   w.m = at - w.tn * w.tiles;
   return w;
 }

@@ -112,8 +112,8 @@ gemm_epi_status gemm_epi_group_rows(const int32_t* ids, int64_t rows, int64_t gr
  * belongs to group g and is entry q = order[i] (order NULL: q = i).  Both arrays
  * are in device memory and are read when the kernel runs, so a captured graph
  * follows what they hold at its replay.  Offsets are taken as clamped to [0,
- * rows], an order outside [0, rows) is no entry, and a group whose end lies
- * before its beginning has none. */
+ * rows] and as no lower than any before them, so that no place is of two groups;
+ * an order outside [0, rows) is no entry. */
 typedef struct gemm_epi_groups {
   const int32_t* offsets; /* [groups + 1] */
   const int32_t* order;   /* [rows] or NULL */

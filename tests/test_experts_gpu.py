@@ -415,6 +415,54 @@ def test_grouped_gemm_of_any_offsets_and_order():
         assert float(torch.stack([(got[r] - y).abs() for y in either]).amin(0).max()) < 0.05, r
 
 
+# Offsets that do not ascend, whose ranges as written would overlap in more tiles
+# than the rows and groups of ascending ones have: a case for each of the kernels.
+OVERLAPS = [("stream", 64, 16, 300, 4112), ("64x64_two", 1024, 8, 256, 272), ("64x64_four", 400, 16, 128, 2064),
+            ("128x128", 3200, 40, 1000, 1040), ("128x128_four", 1280, 20, 1100, 4112), ("256x256", 2560, 10, 4700, 2064),
+            ("many_groups", 700, 1000, 40, 144), ("many_groups_stream", 500, 300, 40, 4112)]
+
+
+@pytest.mark.parametrize("name,rows,groups,cols,row", OVERLAPS, ids=[k[0] for k in OVERLAPS])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("offsets", ["jumps", "steps"])
+def test_grouped_gemm_of_offsets_that_descend(name, rows, groups, cols, row, dtype, gated, offsets):
+    """Offsets count as no lower than any before them: each place that is then
+    named has its group's value, the others stay as they were."""
+    g = torch.Generator(device="cuda").manual_seed(rows + groups)
+    K, N, out = row // (1 if dtype == "i8" else 2), cols // (2 if gated else 1), "bf16" if dtype == "i8" else dtype
+    cols, xs, ws = N * (2 if gated else 1), None, None
+    if dtype == "i8":
+        x = torch.randint(-128, 128, (rows, K), generator=g, dtype=torch.int8, device="cuda")
+        w = torch.randint(-128, 128, (groups, cols, K), generator=g, dtype=torch.int8, device="cuda")
+        xs = torch.rand(rows, generator=g, device="cuda") * 2.0 ** -7
+        ws = torch.rand(groups, cols, generator=g, device="cuda") / K ** 0.5 * 2.0 ** -5
+    else:
+        x = torch.randn(rows, K, generator=g, device="cuda").to(DT[dtype])
+        w = (torch.randn(groups, cols, K, generator=g, device="cuda") * K ** -0.5).to(DT[dtype])
+    if offsets == "jumps":  # to and fro between the first rows and the last
+        low = torch.randint(3, rows // 8, (groups // 2 + 1,), generator=gen(rows))
+        high = torch.randint(rows // 2, rows - 3, (groups // 2 + 1,), generator=gen(groups))
+        off = torch.stack([low, high], 1).reshape(-1)[:groups + 1]
+    else:  # up, but for some that fall back, one far below 0
+        off = 5 + torch.arange(groups + 1) * (rows - 11) // groups
+        back = torch.randint(1, groups, (groups // 4,), generator=gen(groups))
+        off[back] -= torch.randint(1, rows // 2, (groups // 4,), generator=gen(rows))
+        off[back[0]] = -(1 << 31)
+    epilogue = "silu" if gated else "none"
+    c, _ = blank(rows, N, out)
+    gb.grouped_gemm(x, w, c, off.int().cuda(), gated=gated, epilogue=epilogue, x_scale=xs, w_scale=ws)
+    raised = off.clamp(0, rows).cummax(0).values.tolist()
+    for e in range(groups):
+        i = slice(raised[e], raised[e + 1])
+        if i.start == i.stop:
+            continue
+        z, lost = pre(x[i], w[e], None if xs is None else xs[i], None if ws is None else ws[e], None)
+        y, t = post(z[:, :N], lost[:, :N], epilogue, out, (z[:, N:], lost[:, N:]) if gated else None)
+        within(c[i], y.cpu(), t.cpu(), f"{name} group {e}")
+    assert bool(c[:raised[0]].isnan().all()) and bool(c[raised[-1]:].isnan().all()), "rows that no range names written"
+
+
 def test_an_order_counts_where_nothing_is_gathered_or_scattered():
     x, w = rand(gen(1), 8, 64, dtype="bf16"), rand(gen(2), 1, 16, 64, dtype="bf16")
     order = torch.tensor([3, -1, 0, 8, 5, 6, 7, 1], dtype=torch.int32)
