@@ -509,6 +509,59 @@ def test_rows_far_apart():
     assert torch.equal(q.cpu(), qw) and same_scale(s, sw)
 
 
+def test_products_of_rows_16_mib_apart():
+    """The largest distance between rows, in both operands: the last rows of a
+    tile lie a GiB behind its first."""
+    g, ld, M, N, K = gen(16), 1 << 24, 70, 66, 4112
+    a, b, r = codes(g, M, K), codes(g, N, K), rand(g, M, N, dtype="bf16")
+    xs, ws = torch.rand(M, generator=g) * 2.0 ** -8, torch.rand(N, generator=g) * 2.0 ** -10
+    far = [torch.empty((n - 1) * ld + K, dtype=torch.int8, device="cuda").as_strided((n, K), (ld, 1)) for n in (M, N)]
+    far[0].copy_(a)
+    far[1].copy_(b)
+    for m in (16, M):  # (streamed, and in tiles)
+        z, lost = pre(a[:m], b, xs[:m], ws, None)
+        c, _ = blank(m, N, "bf16")
+        gb.i8_gemm(far[0][:m], xs[:m].cuda(), far[1], ws.cuda(), c, residual=r[:m].cuda())
+        within(c, *post(z, lost, "none", "bf16", residual=r[:m]), f"{m} rows")
+
+
+@pytest.mark.parametrize("name,rows,ld,K,groups", [("tiles", 65534, 32760, 32760, 1), ("stream", 4095, 1 << 19, 2056, 1024)])
+def test_gathered_rows_up_to_4_gib(name, rows, ld, K, groups):
+    """A gathered X just below the largest one: its first and last rows."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.zeros(rows * ld, dtype=torch.bfloat16, device="cuda").as_strided((rows, K), (ld, 1))
+    q = torch.tensor([rows - 1, 0, rows // 2, rows - 2], device="cuda")
+    x[q] = torch.randn(4, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(groups, 24, K, generator=g, device="cuda") * K ** -0.5).to(torch.bfloat16)
+    off = torch.full((groups + 1,), 4, dtype=torch.int32, device="cuda")
+    off[0] = 0  # all of group 0
+    order = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    order[:4] = q.int()
+    c, _ = blank(rows, 24, "bf16")
+    gb.grouped_gemm(x, w, c, off, order, gather=True)
+    z, lost = pre(x[q], w[0], None, None, None)
+    y, t = post(z, lost, "none", "bf16")
+    within(c[:4], y.cpu(), t.cpu(), name)
+    assert bool(c[4:].isnan().all())
+
+
+@pytest.mark.parametrize("rows", [3, 20, 200])
+def test_gates_of_2_gib(rows):
+    """The most that a group's gates may have: its values lie 2 GiB behind."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    N, K = 1 << 14, 1 << 16
+    x = torch.randn(rows, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.empty(1, 2 * N, K, dtype=torch.bfloat16, device="cuda").normal_(0.0, K ** -0.5, generator=g)
+    c, _ = blank(rows, N, "bf16")
+    gb.grouped_gemm(x, w, c, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), gated=True, epilogue="silu")
+    assert bool(c.isfinite().all())
+    for at in (0, N // 2 - 32, N - 64):
+        n = torch.arange(at, at + 64, device="cuda")
+        z, lost = pre(x, w[0][n], None, None, None)
+        y, t = post(z, lost, "silu", "bf16", pre(x, w[0][n + N], None, None, None))
+        within(c[:, at:at + 64], y.cpu(), t.cpu(), f"columns from {at}")
+
+
 # ---- the router --------------------------------------------------------------------
 
 def route_want(logits, per, score, renormalise, scale):
