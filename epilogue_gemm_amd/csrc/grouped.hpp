@@ -8,19 +8,21 @@
 // layout in LDS serves both:
 //   * tile_kernel: tiles of 64 x 64 to 256 x 256, rows of X gathered by the direct
 //     copies themselves, the group found by each workgroup from the offsets.  Large
-//     ones are bound by the power limit (i8 8192^3 398 to 420 us, 2.6 to 2.8 POP/s
-//     at some 1.95 GHz with the matrix units 67 % busy; bf16, 8 groups of 16384
-//     rows, 2 x 4096 of 4096, 862 us, 1.28 PFLOP/s), those of short K by the
-//     epilogue and the lookups (32 groups of 12284 rows, 4096 of 2048, i8: 160 us,
-//     of which the matrix units are busy 41 %), small ones by the latency of a
-//     k-step;
+//     ones are bound by the power limit (i8 8192^3 398 to 440 us, 2.5 to 2.8 POP/s;
+//     under counters 467 us at 1.77 GHz of 2.4 with the matrix units 67 % busy;
+//     bf16, 8 groups of 16384 rows, 2 x 4096 of 4096, 860 to 900 us, 1.22 to 1.28
+//     PFLOP/s, 925 us at 1.78 GHz, 72 %), those of short K by the epilogue and the
+//     lookups (32 groups of 12284 rows, 4096 of 2048, i8: 159 to 164 us, of which the
+//     matrix units are busy 41 %), small ones by the latency of a k-step (1001 x 2055
+//     x 4096, i8: 21 to 22 us for 32 of them, 21 % busy);
 //   * stream_kernel: for few rows a group, bound by W from HBM (32 tokens, 4 of 64,
-//     2 x 1024 of 2048, bf16: 80.5 us, 5.9 TB/s, 1.00 x the least bytes).
+//     2 x 1024 of 2048, bf16: 80.0 us, 6.0 TB/s, 1.00 x the least bytes).
 // Measured and not kept: a workgroup a tile of the streaming kernel (83.9 us for
 // 80.5), twice its ring with one workgroup a CU (82.8), 32 or 64 rows a tile there
 // (X as operands for rows that mostly are none: 88.7, 105); 128 x 256 tiles of three
 // stages (531 us for 398 at 8192^3); 64 x 64 with eight stages, a workgroup a CU
-// (the same for few tiles, 65 us for 52 at 2048 x 4096 x 4096); the epilogue's
+// (i8, 64 x 2048 x 8192 13.5 us for 13.5, 32 rows 12.1 for 12.9; 1024 x 2560 x 4096
+// 24.4 for 20.0, 2048 x 4096 x 4096 65 for 52); the epilogue's
 // bands staged apart, each stored while the next one is formed (164 us for 160
 // in 12284 rows of 32 groups).
 #pragma once
@@ -834,18 +836,25 @@ hipError_t launch_stream(Args a, bool gated, hipStream_t stream) {
 // CUs.  Measured (us; W past the caches where it has 128 MiB):
 //   stream: up to 4 rows a group (16 of a single one) and K of 4 KiB.  2 rows, 64
 //     groups of 2 x 1024 x 2048 bf16 80.3, 64 x 64 88.0; K of 2 KiB 43.2 and 40.7.
-//   256 x 256: more than 96 rows, K of 2 KiB, tiles for most CUs.  i8 4096 x 4096 x
-//     4096 53.8, 128 x 128 68.3; K of 1 KiB 33.6 and 32.4; 2048 x 4096 x 4096 44.0
-//     and 35.9; 32 groups of 512 rows x 2048 x 1024 bf16 97.2 and 104; 64 rows a
-//     group 131 and 126.
+//     i8, 16 x 2048 x 8192 10.1 and 12.4, 16 x 4096 x 4096 7.5 and 8.3.  (Its tiles
+//     of 16 rows are the faster ones for more rows too while few columns leave
+//     CUs idle: 64 x 2048 x 8192 10.3 and 13.5, 32 x 4096 x 4096 7.5 and 8.5, but 64 x
+//     4096 x 4096 10.1 and 8.9, 64 x 8192 x 8192 39.3 and 14.8.)
+//   256 x 256: more than 96 rows, K of 2 KiB, tiles for most CUs (more than 176 of
+//     256; 192 tiles, i8 2880 x 4096 x 2048 31.2, 128 x 128 32.8; 176, 2816 rows 30.6
+//     and 32.7, and 2048 x 5632 x 4096 48.0 and 56.4: the border could be lower).  i8
+//     4096 x 4096 x 4096 53.8, 128 x 128 68.3; K of 1 KiB 33.6 and 32.4; 2048 x 4096 x
+//     4096 44.0 and 35.9; 32 groups of 512 rows x 2048 x 1024 bf16 97.2 and 104; 64
+//     rows a group 131 and 126.
 //   128 x 128, two a CU: more than 48 rows, K of 1 KiB, more than one a CU.  i8 4096
 //     x 4096 x 1024 32.4, 64 x 64 38.9; K of 256 24.7 and 24.5; 32 rows a group 122
-//     and 94.5.  Of four stages where one a CU is enough for all: 1024 x 4096 x 4096
-//     21.1, of two stages 25.2, 64 x 64 26.5; 1001 x 2055 x 4096 23.0 and (64 x 64)
-//     20.7.
+//     and 94.5.  Of four stages where one a CU is enough for all, more than 160:
+//     1024 x 4096 x 4096 21.1, of two stages 25.2, 64 x 64 26.5; 1024 x 2560 x 4096, 160
+//     tiles, 17.6 and (64 x 64) 19.5, 512 x 4096 x 4096, 128 tiles, 17.3 and 15.2: the
+//     border could be lower by some tiles.
 //   64 x 64: the rest, four a CU of two stages where there are many (and K below 4
 //     KiB, or more than 48 rows) or K is short, else two of four stages.  i8 1001 x
-//     2055 x 4096 20.7 and 22.3; 7252 x 470 x 176 7.7 and 11.0, 128 x 128 13.3; 256
+//     2055 x 4096 20.7 and 22.3, 800 x 4096 x 4096 25.7 and 25.6; 7252 x 470 x 176 7.7 and 11.0, 128 x 128 13.3; 256
 //     x 4096 x 4096 16.9 and 9.5; 32 rows a group of K of 4 KiB 121 and 94.6.
 // Weights of 128 MiB and more are read past the caches (64 x 64, 32 rows: 94.5 for
 // 107.7), unless a group's many rows read them often (2048 rows, 862 for 876);

@@ -38,7 +38,8 @@ extern "C" {
  *   Y      rows x cols (ldy), 8-bit integers
  *   scale  rows fp32 values
  * A row that holds an infinity or a NaN gets scale NaN and zeros (all its
- * values read as NaN).  Y and scale overlap nothing else.  Any alignment of an
+ * values read as NaN, and its products are NaN, of which a ReLU, max(z, 0),
+ * makes 0).  Y and scale overlap nothing else.  Any alignment of an
  * element.  rows = 0 does nothing.
  * Errors: INVALID_ARG (a NULL pointer, rows < 0, cols <= 0, a leading
  * dimension below cols, dtype not F16 or BF16, a pointer off its element's
