@@ -587,8 +587,9 @@ def group_rows(ids, offsets, order, stream=None):
 
 def grouped_gemm(x, w, c, offsets, order=None, per=1, gather=False, scatter=False, gated=False, bias=None,
                  epilogue="none", x_scale=None, w_scale=None, stream=None):
-    """For place i of group g, offsets[g] <= i < offsets[g + 1], and entry q =
-    order[i] (without ``order``: i): row q of c (``scatter``, else row i) = act(row
+    """For place i of group g, offsets[g] <= i < offsets[g + 1] (offsets that
+    descend count as no lower than any before them), and entry q = order[i]
+    (without ``order``: i): row q of c (``scatter``, else row i) = act(row
     q // per of x (``gather``, else row i) w[g]^T + bias[g]).  w [groups, N, K],
     and with ``gated`` [groups, 2 N, K], N rows of gates, then N of values: act(x
     gate^T + bias) * (x value^T + bias).  c [rows, N], x [rows, K], or with ``gather``
